@@ -388,6 +388,183 @@ MOE_API moe_status moe_backward(const moe_config *cfg, const void *x, const floa
  */
 MOE_API int32_t moe_backward_kernel_count(const moe_config *cfg);
 
+/* ------------------------------------------------------ around the layer
+ *
+ * What a transformer block does beside the layer: the residual addition and
+ * root-mean-square norm before it ("2.9 Mixture-of-Experts (MoE)
+ * Architectures": the layer stands where a dense block's FFN stands, behind the
+ * same norm), balance losses over the sequences of a padded batch, and experts
+ * held in 8 bits.
+ *
+ * 8-bit data ("mx8"): e4m3 values in blocks of 32 along the contracted axis,
+ * one scale byte b per block standing for 2^(b - 127); an element's value is
+ * e4m3 * 2^(b - 127).  Where this library quantises, the scale is the least
+ * power of two with max|v| <= 448 * scale (a block of zeros: byte 0), elements
+ * are rounded to nearest even, and a block that holds an infinity or a NaN
+ * becomes NaN as a whole (byte 255, elements 0x7f).  Data from elsewhere may
+ * use any scales.  Rows of n elements are n bytes, their scales n / 32 bytes,
+ * both dense and row-major.
+ */
+
+/*
+ * Residual addition and root-mean-square norm of T rows of D elements (dtype:
+ * moe_dtype):
+ *   s = x + residual, rounded to dtype (x itself without a residual)
+ *   rstd[t] = (mean_d s[t,d]^2 + eps)^(-1/2)
+ *   n[t,d] = s[t,d] * rstd[t] * gamma[d], rounded to dtype
+ *   q, q_scales = n as mx8 rows
+ * x is required, residual (T, D) may be NULL; gamma (D) fp32; eps >= 0.
+ * Outputs, each NULL to skip: s (T, D; only with a residual: MOE_ERR_ARG
+ * otherwise), n (T, D), rstd (T) fp32, q (T, D bytes) with q_scales
+ * (T, D / 32 bytes; both or neither, D a multiple of 32: MOE_ERR_ALIGN
+ * otherwise).  n or q is required.  Squares are summed in fp32.  s and n may be
+ * the memory of x or of residual (not each other's).  D <= 65536
+ * (MOE_ERR_UNSUPPORTED), T < 2^31.  A row that holds an infinity or NaN gives
+ * what the formulas give; no other row is touched by it.
+ */
+MOE_API moe_status moe_rmsnorm(int64_t T, int32_t D, int32_t dtype, const void *x, const void *residual,
+                               const float *gamma, float eps, void *s, void *n, float *rstd, void *q,
+                               void *q_scales, void *stream);
+
+/* Bytes of device scratch moe_rmsnorm_backward needs. */
+MOE_API moe_status moe_rmsnorm_backward_workspace_size(int64_t T, int32_t D, size_t *bytes);
+
+/*
+ * Backward of moe_rmsnorm for the upstream gradients dn of n and ds of s (NULL:
+ * none), with the forward's s (x where there was no residual) and rstd:
+ *   g = dn * gamma,  xh = s * rstd
+ *   dx[t,d]  = ds[t,d] + rstd[t] * (g[t,d] - xh[t,d] * mean_d'(g xh)),
+ *              rounded to dtype; the gradient of x and of residual alike
+ *   dgamma[d] = sum_t dn[t,d] * xh[t,d]   (fp32, overwritten)
+ * dx may be the memory of dn or ds.  Sums are fp32, in an order fixed by the
+ * shape.  workspace: moe_rmsnorm_backward_workspace_size bytes, 256-byte aligned.
+ */
+MOE_API moe_status moe_rmsnorm_backward(int64_t T, int32_t D, int32_t dtype, const void *dn, const void *ds,
+                                        const void *s, const float *gamma, const float *rstd, void *dx,
+                                        float *dgamma, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rows into mx8 and back.  rows x cols elements of dtype, cols a multiple of 32
+ * (MOE_ERR_ALIGN); q rows * cols bytes, scales rows * cols / 32 bytes.
+ * moe_mx8_dequantize rounds the values once to dtype (exact but below bf16's or
+ * fp32's least values).
+ */
+MOE_API moe_status moe_mx8_quantize(int64_t rows, int32_t cols, int32_t dtype, const void *x, void *q,
+                                    void *scales, void *stream);
+MOE_API moe_status moe_mx8_dequantize(int64_t rows, int32_t cols, int32_t dtype, const void *q,
+                                      const void *scales, void *out, void *stream);
+
+/*
+ * Expert weights w (E, K, N) of dtype, contracted over K, into the layout of the
+ * 8-bit experts: q (E, N, K) bytes and scales (E, N, K / 32) bytes, blocks of 32
+ * along K.  K a multiple of 32, N of 8.  Once per weight value.
+ */
+MOE_API moe_status moe_mx8_prepare_weight(int32_t E, int32_t K, int32_t N, int32_t dtype, const void *w,
+                                          void *q, void *scales, void *stream);
+
+/* The experts' 8-bit weights (device pointers, 16-byte aligned):
+ * gate, up (E, F, D) with scales (E, F, D / 32); down (E, D, F) with (E, D, F / 32). */
+typedef struct moe_mx8_weights {
+    const void *gate, *gate_scales;
+    const void *up, *up_scales;
+    const void *down, *down_scales;
+} moe_mx8_weights;
+
+/* Bytes of device workspace moe_expert_ffn_mx8 needs (256-byte aligned, zeroed
+ * once before first use; its first word is the device status word). */
+MOE_API moe_status moe_mx8_workspace_size(const moe_config *cfg, size_t *bytes);
+
+/*
+ * moe_expert_ffn on 8-bit rows and weights.  cfg->dtype is MOE_BF16 (the type of
+ * y_perm; MOE_ERR_UNSUPPORTED otherwise), D and F multiples of 32
+ * (MOE_ERR_ALIGN).  For every row r < offsets[E] of expert e:
+ *   h[r, :]      = silu(x[r] Wg_e) * (x[r] Wu_e), rounded from fp32 to mx8
+ *                  (blocks of 32 along F)
+ *   y_perm[r, :] = topk_w[perm[r]] * (h[r] Wd_e)                  (bf16)
+ * xq (max_rows, D) and xs (max_rows, D / 32): expert-major rows as mx8; hq
+ * (max_rows, F) and hs (max_rows, F / 32): the intermediate, written here.
+ * perm and topk_w may both be NULL (weight 1).  Rows at and behind offsets[E]
+ * are left as they were.  A NaN scale makes the rows that meet it NaN.
+ */
+MOE_API moe_status moe_expert_ffn_mx8(const moe_config *cfg, const void *xq, const void *xs,
+                                      const int32_t *offsets, const int32_t *perm, const float *topk_w,
+                                      const moe_mx8_weights *weights, void *hq, void *hs, void *y_perm,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace moe_forward_mx8 needs. */
+MOE_API moe_status moe_forward_mx8_workspace_size(const moe_config *cfg, size_t *bytes);
+
+/*
+ * moe_forward with the experts in 8 bits: moe_route on x (bf16), moe_dispatch,
+ * a gather of the 8-bit rows, moe_expert_ffn_mx8, moe_combine.  xq, xs: x as mx8
+ * rows (moe_rmsnorm's q and q_scales, say); both NULL: x is quantised into the
+ * workspace first.  y_add (T, D) bf16 or NULL is added to the output.  The
+ * routing arguments and optional outputs are moe_forward's.  A shared expert is
+ * not supported here (cfg->F_shared must be 0: MOE_ERR_UNSUPPORTED).
+ */
+MOE_API moe_status moe_forward_mx8(const moe_config *cfg, const void *x, const void *xq, const void *xs,
+                                   const float *w_router, const void *w_router_terms, const float *router_bias,
+                                   const float *selection_bias, const float *logit_noise,
+                                   const moe_mx8_weights *weights, const void *y_add, void *y, float *losses,
+                                   float *mean_prob, int32_t *counts, int32_t *topk_ids, float *topk_w,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace moe_balance_loss needs for S sequences. */
+MOE_API moe_status moe_balance_workspace_size(const moe_config *cfg, int64_t S, size_t *bytes);
+
+/*
+ * Balance loss, z-loss and per-expert counts over the sequences of a batch, with
+ * the gradient of the routing logits ("2.9 Mixture-of-Experts (MoE)
+ * Architectures", "The auxiliary load-balancing loss", taken per sequence and
+ * over the tokens that count).
+ *   seq_starts (S + 1) int32, device: sequence i is the tokens seq_starts[i] ..
+ *   seq_starts[i+1] - 1; non-decreasing, within 0 .. T (else the workspace's
+ *   bounds flag).  Sequences may be empty; tokens outside all of them do not
+ *   count.  token_mask (T) bytes or NULL: a token whose byte is 0 does not count.
+ *   With n_i counted tokens in sequence i, S' sequences that have any, N in all,
+ *   p the scores of moe_route (softmax, or the normalised sigmoid):
+ *   counts[i,e] = #{(t,k): t counts in i, topk_ids[t,k] = e}       (S, E) int32
+ *   seq_loss[i] = E * sum_e counts[i,e] / (n_i K) * mean_t p[t,e]   (S) fp32
+ *   losses[0] = z-loss = (1/N) sum_t (logsumexp_e logits[t,e])^2
+ *   losses[1] = balance = (1/S') sum_i seq_loss[i]
+ *   dlogits[t,:] = gradient of c_balance * losses[1] + c_z * losses[0] (the
+ *   counts carry none); zero for a token that does not count   (T, E) fp32
+ * All are overwritten; dlogits may be NULL.  With no counted token the losses are
+ * 0.  Logits of tokens that do not count are not read.  A counted token's NaN
+ * shows in its sequence's loss, the losses and its own gradient.  An id outside
+ * 0 .. E - 1 raises the bounds flag and is not counted.  Bit-reproducible.
+ * logits (T, E) fp32 and topk_ids (T, K) as moe_route writes them; the fields
+ * T, E, K and score_func of cfg are used.  S >= 1, S * E < 2^31.  workspace:
+ * 256-byte aligned, zeroed once before first use.
+ */
+MOE_API moe_status moe_balance_loss(const moe_config *cfg, int64_t S, const float *logits,
+                                    const int32_t *topk_ids, const int32_t *seq_starts,
+                                    const uint8_t *token_mask, float c_balance, float c_z, int32_t *counts,
+                                    float *losses, float *seq_loss, float *dlogits, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * Byte offsets, within moe_forward_train's state, of the routed logits (T, E)
+ * fp32 and of the selected ids (T, K) int32: what moe_balance_loss reads.
+ * Host-only.
+ */
+MOE_API moe_status moe_train_state_router(const moe_config *cfg, size_t *logits_offset, size_t *ids_offset);
+
+/*
+ * moe_backward with a further gradient of the routing logits: dlogits_add (T, E)
+ * fp32 (moe_balance_loss's dlogits, say; NULL: none) is added to the layer's own
+ * before it goes on to the router weight, its bias and dx.
+ */
+MOE_API moe_status moe_backward_aux(const moe_config *cfg, const void *x, const float *w_router,
+                                    const void *w_gate, const void *w_up, const void *w_down,
+                                    const void *w_gate_shared, const void *w_up_shared,
+                                    const void *w_down_shared, const void *state, size_t state_bytes,
+                                    const void *dy, float c_balance, float c_z, const float *dlogits_add,
+                                    void *dx, float *dw_router, float *db_router, float *dw_gate,
+                                    float *dw_up, float *dw_down, float *dw_gate_shared,
+                                    float *dw_up_shared, float *dw_down_shared, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------- expert parallelism
  *
  * "Lab: build a tiny MoE in PyTorch", "From local loop to expert

@@ -99,7 +99,25 @@ _SIG = {
     "moe_backward_workspace_size": ([_P, _P], ctypes.c_int32),
     "moe_backward": ([_P] * 10 + [ctypes.c_size_t, _P, ctypes.c_float, ctypes.c_float]
                      + [_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_backward_aux": ([_P] * 10 + [ctypes.c_size_t, _P, ctypes.c_float, ctypes.c_float]
+                         + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_train_state_router": ([_P] * 3, ctypes.c_int32),
     "moe_backward_kernel_count": ([_P], ctypes.c_int32),
+    "moe_rmsnorm": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32] + [_P] * 3 + [ctypes.c_float]
+                    + [_P] * 6, ctypes.c_int32),
+    "moe_rmsnorm_backward_workspace_size": ([ctypes.c_int64, ctypes.c_int32, _P], ctypes.c_int32),
+    "moe_rmsnorm_backward": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32] + [_P] * 8
+                             + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_mx8_quantize": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32] + [_P] * 4, ctypes.c_int32),
+    "moe_mx8_dequantize": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32] + [_P] * 4, ctypes.c_int32),
+    "moe_mx8_prepare_weight": ([ctypes.c_int32] * 4 + [_P] * 4, ctypes.c_int32),
+    "moe_mx8_workspace_size": ([_P, _P], ctypes.c_int32),
+    "moe_expert_ffn_mx8": ([_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_forward_mx8_workspace_size": ([_P, _P], ctypes.c_int32),
+    "moe_forward_mx8": ([_P] * 18 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_balance_workspace_size": ([_P, ctypes.c_int64, _P], ctypes.c_int32),
+    "moe_balance_loss": ([_P, ctypes.c_int64] + [_P] * 4 + [ctypes.c_float, ctypes.c_float] + [_P] * 5
+                         + [ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_trace_attach_backward": ([_P, ctypes.c_int32], ctypes.c_int32),
     "moe_trace_backward_boundary_count": ([], ctypes.c_int32),
     "moe_trace_backward_stage_name": ([ctypes.c_int32], ctypes.c_char_p),
@@ -320,14 +338,15 @@ def moe_forward_train(cfg, x, w_router, w_gate, w_up, w_down, y, state, router_b
 
 def moe_backward(cfg, x, w_router, w_gate, w_up, w_down, state, dy, dx, dw_router, dw_gate, dw_up,
                  dw_down, workspace, c_balance: float = 0.0, c_z: float = 0.0, db_router=None,
-                 shared=None, dshared=None, stream=None):
+                 shared=None, dshared=None, stream=None, dlogits_add=None):
     """shared = (w_gate_s, w_up_s, w_down_s) and dshared = their fp32
-    gradient buffers when cfg.F_shared > 0."""
+    gradient buffers when cfg.F_shared > 0.  dlogits_add (T, E) fp32: a further
+    gradient of the routing logits (moe_balance_loss's)."""
     sg, su, sd = shared if shared is not None else (None, None, None)
     dg, du, dd = dshared if dshared is not None else (None, None, None)
-    st = lib().moe_backward(_cfg(cfg), _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up),
+    st = lib().moe_backward_aux(_cfg(cfg), _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up),
                             _ptr(w_down), _ptr(sg), _ptr(su), _ptr(sd), _ptr(state), _nbytes(state),
-                            _ptr(dy), float(c_balance), float(c_z), _ptr(dx), _ptr(dw_router),
+                            _ptr(dy), float(c_balance), float(c_z), _ptr(dlogits_add), _ptr(dx), _ptr(dw_router),
                             _ptr(db_router), _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), _ptr(dg),
                             _ptr(du), _ptr(dd), _ptr(workspace), _nbytes(workspace),
                             _stream(stream))
@@ -417,6 +436,248 @@ def _nbytes(t) -> int:
     if isinstance(t, int):
         raise ValueError("pass the workspace as a tensor so its size is known")
     return t.numel() * t.element_size()
+
+
+# ------------------------------------------------------------ around the layer
+#
+# These take torch tensors only, and check each one's device, type, size and
+# layout before its address goes to the library: a wrong tensor is a ValueError,
+# what the library itself refuses a MoEError.  The work goes to the given
+# stream, or to the current stream of the tensors' device.
+
+def _check_tensors(where, specs):
+    """specs: (name, tensor or None, dtype names, elements).  Returns the device
+    index they share."""
+    import torch
+    dev = None
+    for name, t, dtypes, numel in specs:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{where}: {name} must be a tensor")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{where}: {name} has dtype {t.dtype}")
+        if t.numel() != numel:
+            raise ValueError(f"{where}: {name} has {t.numel()} elements, expected {numel}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{where}: {name} is on another device than the other tensors")
+    if dev is None or dev < 0:
+        raise ValueError(f"{where}: the tensors must be on a CUDA device")
+    return dev
+
+
+def _run(where, dev, fn, args, stream):
+    """fn(*args, stream) on device dev."""
+    import torch
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    if st != MOE_OK:
+        raise MoEError(st, where)
+
+
+def _layer_types():
+    import torch
+    return {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+_TYPES = None
+
+
+def _types():
+    """(layer dtypes -> moe_dtype, fp32, int32, the dtypes of 8-bit values, of bytes)"""
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = (_layer_types(), (torch.float32,), (torch.int32,), (torch.float8_e4m3fn, torch.uint8),
+                  (torch.uint8, torch.bool, torch.float8_e8m0fnu))
+    return _TYPES
+
+
+def _rows(where, name, t, layer):
+    if getattr(t, "dim", None) is None or t.dim() != 2 or t.dtype not in layer:
+        raise ValueError(f"{where}: {name} must be a (rows, columns) bf16 or fp32 tensor")
+    return t.shape[0], t.shape[1], (t.dtype,)
+
+
+def moe_rmsnorm(x, gamma, n, residual=None, s=None, rstd=None, q=None, q_scales=None, eps: float = 1e-6,
+                stream=None):
+    """s = x + residual; n = s * (mean s^2 + eps)^(-1/2) * gamma; q, q_scales = n as
+    mx8 rows (include/moe.h).  x (T, D) bf16 or fp32, gamma (D) fp32; the outputs
+    n, s, rstd (T) fp32, q (T, D) e4m3 or bytes, q_scales (T, D / 32) are the
+    caller's buffers, each optional (n or q is required; s needs a residual)."""
+    layer, f32, _, q8, byte = _types()
+    T, D, dt = _rows("moe_rmsnorm", "x", x, layer)
+    nel = T * D
+    dev = _check_tensors("moe_rmsnorm", (
+        ("x", x, dt, nel), ("gamma", gamma, f32, D), ("n", n, dt, nel), ("residual", residual, dt, nel),
+        ("s", s, dt, nel), ("rstd", rstd, f32, T), ("q", q, q8, nel), ("q_scales", q_scales, byte, nel // 32)))
+    _run("moe_rmsnorm", dev, lib().moe_rmsnorm,
+         (T, D, layer[x.dtype], _ptr(x), _ptr(residual), _ptr(gamma), eps, _ptr(s), _ptr(n), _ptr(rstd), _ptr(q),
+          _ptr(q_scales)), stream)
+
+
+def rmsnorm_backward_workspace_size(T: int, D: int) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().moe_rmsnorm_backward_workspace_size(int(T), int(D), ctypes.byref(v)),
+           "moe_rmsnorm_backward_workspace_size")
+    return v.value
+
+
+def moe_rmsnorm_backward(dn, s, gamma, rstd, dx, dgamma, workspace, ds=None, stream=None):
+    """Gradients of moe_rmsnorm: dx (of x and of the residual alike) and dgamma (D)
+    fp32 from dn (of n) and ds (of s, or None), with the forward's s and rstd."""
+    layer, f32, _, _, byte = _types()
+    T, D, dt = _rows("moe_rmsnorm_backward", "s", s, layer)
+    nel = T * D
+    dev = _check_tensors("moe_rmsnorm_backward", (
+        ("s", s, dt, nel), ("dn", dn, dt, nel), ("gamma", gamma, f32, D), ("rstd", rstd, f32, T),
+        ("dx", dx, dt, nel), ("dgamma", dgamma, f32, D), ("ds", ds, dt, nel),
+        ("workspace", workspace, byte, workspace.numel())))
+    _run("moe_rmsnorm_backward", dev, lib().moe_rmsnorm_backward,
+         (T, D, layer[s.dtype], _ptr(dn), _ptr(ds), _ptr(s), _ptr(gamma), _ptr(rstd), _ptr(dx), _ptr(dgamma),
+          _ptr(workspace), workspace.numel()), stream)
+
+
+def moe_mx8_quantize(x, q, scales, stream=None):
+    """x (rows, cols) bf16 or fp32 into q (rows, cols) e4m3 and scales (rows, cols / 32)."""
+    layer, _, _, q8, byte = _types()
+    T, D, dt = _rows("moe_mx8_quantize", "x", x, layer)
+    dev = _check_tensors("moe_mx8_quantize", (
+        ("x", x, dt, T * D), ("q", q, q8, T * D), ("scales", scales, byte, T * D // 32)))
+    _run("moe_mx8_quantize", dev, lib().moe_mx8_quantize,
+         (T, D, layer[x.dtype], _ptr(x), _ptr(q), _ptr(scales)), stream)
+
+
+def moe_mx8_dequantize(q, scales, out, stream=None):
+    """The values of q (rows, cols) and scales (rows, cols / 32) into out, bf16 or fp32."""
+    layer, _, _, q8, byte = _types()
+    T, D, dt = _rows("moe_mx8_dequantize", "out", out, layer)
+    dev = _check_tensors("moe_mx8_dequantize", (
+        ("out", out, dt, T * D), ("q", q, q8, T * D), ("scales", scales, byte, T * D // 32)))
+    _run("moe_mx8_dequantize", dev, lib().moe_mx8_dequantize,
+         (T, D, layer[out.dtype], _ptr(q), _ptr(scales), _ptr(out)), stream)
+
+
+def moe_mx8_prepare_weight(w, q, scales, stream=None):
+    """w (E, K, N) bf16 or fp32, contracted over K, into q (E, N, K) e4m3 and scales
+    (E, N, K / 32): the layout of the 8-bit experts."""
+    layer, _, _, q8, byte = _types()
+    if getattr(w, "dim", None) is None or w.dim() != 3 or w.dtype not in layer:
+        raise ValueError("moe_mx8_prepare_weight: w must be an (E, K, N) bf16 or fp32 tensor")
+    E, K, N = w.shape
+    dev = _check_tensors("moe_mx8_prepare_weight", (
+        ("w", w, (w.dtype,), E * K * N), ("q", q, q8, E * K * N), ("scales", scales, byte, E * K * N // 32)))
+    _run("moe_mx8_prepare_weight", dev, lib().moe_mx8_prepare_weight,
+         (E, K, N, layer[w.dtype], _ptr(w), _ptr(q), _ptr(scales)), stream)
+
+
+class Mx8Weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("gate", "gate_scales", "up", "up_scales", "down", "down_scales")]
+
+
+def _mx8_specs(cfg, weights):
+    _, _, _, q8, byte = _types()
+    if len(weights) != 6:
+        raise ValueError("weights: (gate, gate_scales, up, up_scales, down, down_scales)")
+    n = cfg.E * cfg.D * cfg.F
+    return [(name, t, byte if i & 1 else q8, n // 32 if i & 1 else n)
+            for i, ((name, _), t) in enumerate(zip(Mx8Weights._fields_, weights))]
+
+
+def mx8_workspace_size(cfg: MoeConfig) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().moe_mx8_workspace_size(_cfg(cfg), ctypes.byref(v)), "moe_mx8_workspace_size")
+    return v.value
+
+
+def moe_expert_ffn_mx8(cfg, xq, xs, offsets, perm, topk_w, weights, hq, hs, y_perm, workspace, stream=None):
+    """moe_expert_ffn on mx8 rows: xq (max_rows, D), xs (max_rows, D / 32); weights =
+    (gate, gate_scales, up, up_scales, down, down_scales) as moe_mx8_prepare_weight
+    writes them; hq, hs: the intermediate; y_perm (max_rows, D) bf16."""
+    import torch
+    _, f32, i32, q8, byte = _types()
+    R = max_rows(cfg)
+    dev = _check_tensors("moe_expert_ffn_mx8", [
+        ("xq", xq, q8, R * cfg.D), ("xs", xs, byte, R * cfg.D // 32), ("offsets", offsets, i32, cfg.E + 1),
+        ("perm", perm, i32, R), ("topk_w", topk_w, f32, cfg.T * cfg.K), ("hq", hq, q8, R * cfg.F),
+        ("hs", hs, byte, R * cfg.F // 32), ("y_perm", y_perm, (torch.bfloat16,), R * cfg.D),
+        ("workspace", workspace, byte, workspace.numel())] + _mx8_specs(cfg, weights))
+    w = Mx8Weights(*(_ptr(t) for t in weights))
+    _run("moe_expert_ffn_mx8", dev, lib().moe_expert_ffn_mx8,
+         (_cfg(cfg), _ptr(xq), _ptr(xs), _ptr(offsets), _ptr(perm), _ptr(topk_w), ctypes.byref(w), _ptr(hq),
+          _ptr(hs), _ptr(y_perm), _ptr(workspace), workspace.numel()), stream)
+
+
+def forward_mx8_workspace_size(cfg: MoeConfig) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().moe_forward_mx8_workspace_size(_cfg(cfg), ctypes.byref(v)), "moe_forward_mx8_workspace_size")
+    return v.value
+
+
+def moe_forward_mx8(cfg, x, w_router, weights, y, workspace, xq=None, xs=None, y_add=None, router_bias=None,
+                    selection_bias=None, logit_noise=None, w_router_terms=None, losses=None, mean_prob=None,
+                    counts=None, topk_ids=None, topk_w=None, stream=None):
+    """moe_forward with the experts' weights in mx8.  xq, xs: x as mx8 rows (None: x
+    is quantised here); y_add (T, D) is added to the output."""
+    import torch
+    _, f32, i32, q8, byte = _types()
+    T, D, E, K = cfg.T, cfg.D, cfg.E, cfg.K
+    bf16 = (torch.bfloat16,)
+    dev = _check_tensors("moe_forward_mx8", [
+        ("x", x, bf16, T * D), ("w_router", w_router, f32, D * E), ("y", y, bf16, T * D), ("xq", xq, q8, T * D),
+        ("xs", xs, byte, T * D // 32), ("y_add", y_add, bf16, T * D), ("router_bias", router_bias, f32, E),
+        ("selection_bias", selection_bias, f32, E), ("logit_noise", logit_noise, f32, T * E),
+        ("w_router_terms", w_router_terms, byte, router_terms_size(cfg)), ("losses", losses, f32, 3),
+        ("mean_prob", mean_prob, f32, E), ("counts", counts, i32, E), ("topk_ids", topk_ids, i32, T * K),
+        ("topk_w", topk_w, f32, T * K), ("workspace", workspace, byte, workspace.numel())]
+        + _mx8_specs(cfg, weights))
+    w = Mx8Weights(*(_ptr(t) for t in weights))
+    _run("moe_forward_mx8", dev, lib().moe_forward_mx8,
+         (_cfg(cfg), _ptr(x), _ptr(xq), _ptr(xs), _ptr(w_router), _ptr(w_router_terms), _ptr(router_bias),
+          _ptr(selection_bias), _ptr(logit_noise), ctypes.byref(w), _ptr(y_add), _ptr(y), _ptr(losses),
+          _ptr(mean_prob), _ptr(counts), _ptr(topk_ids), _ptr(topk_w), _ptr(workspace), workspace.numel()), stream)
+
+
+def balance_workspace_size(cfg: MoeConfig, S: int) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().moe_balance_workspace_size(_cfg(cfg), int(S), ctypes.byref(v)), "moe_balance_workspace_size")
+    return v.value
+
+
+def moe_balance_loss(cfg, logits, topk_ids, seq_starts, counts, losses, seq_loss, workspace, token_mask=None,
+                     dlogits=None, c_balance: float = 0.0, c_z: float = 0.0, stream=None):
+    """Balance loss and z-loss over the sequences seq_starts (S + 1) int32 of a batch
+    and the tokens whose token_mask (T) byte is not zero: counts (S, E) int32,
+    losses (2) = [z, balance], seq_loss (S), and the gradient dlogits (T, E) of
+    c_balance * balance + c_z * z (include/moe.h)."""
+    _, f32, i32, _, byte = _types()
+    T, E = cfg.T, cfg.E
+    S = seq_starts.numel() - 1
+    dev = _check_tensors("moe_balance_loss", (
+        ("logits", logits, f32, T * E), ("topk_ids", topk_ids, i32, T * cfg.K),
+        ("seq_starts", seq_starts, i32, S + 1), ("counts", counts, i32, S * E), ("losses", losses, f32, 2),
+        ("seq_loss", seq_loss, f32, S), ("token_mask", token_mask, byte, T), ("dlogits", dlogits, f32, T * E),
+        ("workspace", workspace, byte, workspace.numel())))
+    _run("moe_balance_loss", dev, lib().moe_balance_loss,
+         (_cfg(cfg), S, _ptr(logits), _ptr(topk_ids), _ptr(seq_starts), _ptr(token_mask), c_balance, c_z,
+          _ptr(counts), _ptr(losses), _ptr(seq_loss), _ptr(dlogits), _ptr(workspace), workspace.numel()), stream)
+
+
+def train_state_router(cfg: MoeConfig):
+    """Byte offsets of the routed logits (T, E) fp32 and ids (T, K) int32 in a
+    training state."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().moe_train_state_router(_cfg(cfg), ctypes.byref(a), ctypes.byref(b)), "moe_train_state_router")
+    return a.value, b.value
 
 
 # ------------------------------------------------------- expert parallelism

@@ -579,12 +579,12 @@ moe_status moe_backward_workspace_size(const moe_config* cfg, size_t* bytes)
     return MOE_OK;
 }
 
-moe_status moe_backward(const moe_config* cfg, const void* x, const float* w_router,
+moe_status moe_backward_aux(const moe_config* cfg, const void* x, const float* w_router,
                         const void* w_gate, const void* w_up, const void* w_down,
                         const void* w_gate_shared, const void* w_up_shared,
                         const void* w_down_shared, const void* state, size_t state_bytes,
-                        const void* dy, float c_balance, float c_z, void* dx, float* dw_router,
-                        float* db_router, float* dw_gate, float* dw_up, float* dw_down,
+                        const void* dy, float c_balance, float c_z, const float* dlogits_add, void* dx,
+                        float* dw_router, float* db_router, float* dw_gate, float* dw_up, float* dw_down,
                         float* dw_gate_shared, float* dw_up_shared, float* dw_down_shared,
                         void* workspace, size_t workspace_bytes, void* stream)
 {
@@ -600,6 +600,7 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const float* w_rou
             return MOE_ERR_ALIGN;
     }
     if (!isfinite(c_balance) || !isfinite(c_z)) return MOE_ERR_ARG;
+    if (dlogits_add != nullptr && !aligned16(dlogits_add)) return MOE_ERR_ALIGN;
     const moe_config& c = *cfg;
     const int64_t max_rows = max_rows_of(c);
     const TrainLayout TL = train_layout(c, max_rows);
@@ -628,8 +629,8 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const float* w_rou
                                     max_rows, status, s);
     btrace(1, s);
     if (e == cudaSuccess)
-        e = launch_router_bwd(c, logits, ids, row_of, dw_row, cnt, c_balance, c_z, dlogits,
-                              max_rows, status, s);
+        e = launch_router_bwd(c, logits, ids, row_of, dw_row, cnt, c_balance, c_z, dlogits_add,
+                              dlogits, max_rows, status, s);
     btrace(2, s);
     if (e == cudaSuccess)  // dH -> [dg | du], then dXp (boundary 3 between the two)
         e = launch_dgrad(c, max_rows, ws + B.dyp, offsets, sv + TL.gu, w_gate, w_up, w_down,
@@ -669,6 +670,32 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const float* w_rou
         e = launch_dx_assemble(c, dlogits, w_router, ws + B.dxp, row_of, dx_shared, dx, max_rows, s);
     btrace(9, s);
     return cuda_status(e);
+}
+
+moe_status moe_backward(const moe_config* cfg, const void* x, const float* w_router,
+                        const void* w_gate, const void* w_up, const void* w_down,
+                        const void* w_gate_shared, const void* w_up_shared,
+                        const void* w_down_shared, const void* state, size_t state_bytes,
+                        const void* dy, float c_balance, float c_z, void* dx, float* dw_router,
+                        float* db_router, float* dw_gate, float* dw_up, float* dw_down,
+                        float* dw_gate_shared, float* dw_up_shared, float* dw_down_shared,
+                        void* workspace, size_t workspace_bytes, void* stream)
+{
+    return moe_backward_aux(cfg, x, w_router, w_gate, w_up, w_down, w_gate_shared, w_up_shared, w_down_shared,
+                            state, state_bytes, dy, c_balance, c_z, nullptr, dx, dw_router, db_router, dw_gate,
+                            dw_up, dw_down, dw_gate_shared, dw_up_shared, dw_down_shared, workspace,
+                            workspace_bytes, stream);
+}
+
+moe_status moe_train_state_router(const moe_config* cfg, size_t* logits_offset, size_t* ids_offset)
+{
+    moe_status st = check_config(cfg);
+    if (st != MOE_OK) return st;
+    if (logits_offset == nullptr || ids_offset == nullptr) return MOE_ERR_ARG;
+    const TrainLayout L = train_layout(*cfg, max_rows_of(*cfg));
+    *logits_offset = L.logits;
+    *ids_offset = L.f.ids;
+    return MOE_OK;
 }
 
 moe_status moe_update_selection_bias(const moe_config* cfg, const int32_t* counts, float gamma,

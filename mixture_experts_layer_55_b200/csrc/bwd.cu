@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const float* __restrict
                                                          const int32_t* __restrict__ row_of,
                                                          const float* __restrict__ dw_row,
                                                          const int32_t* __restrict__ counts,
+                                                         const float* __restrict__ dlogits_add,
                                                          float* __restrict__ dlogits, int64_t T, int E,
                                                          int K, int score_func, int renorm,
                                                          float route_scale, float c_bal, float c_z,
@@ -205,7 +206,9 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(const float* __restrict
         const int e = lane + 32 * j;
         if (e >= E) continue;
         const float g = sig ? ds[j] * sc[j] * (1.f - sc[j]) : p[j] * (ds[j] - dot2);
-        dlogits[t * E + e] = g + zc * p[j];
+        float d = g + zc * p[j];
+        if (dlogits_add != nullptr) d += dlogits_add[t * E + e];
+        dlogits[t * E + e] = d;
     }
 }
 
@@ -470,12 +473,12 @@ cudaError_t launch_bwd_rows(const moe_config& c, const void* dy, const void* o, 
 
 cudaError_t launch_router_bwd(const moe_config& c, const float* logits, const int32_t* ids,
                               const int32_t* row_of, const float* dw_row, const int32_t* counts,
-                              float c_bal, float c_z, float* dlogits, int64_t max_rows, int* status,
-                              cudaStream_t s)
+                              float c_bal, float c_z, const float* dlogits_add, float* dlogits,
+                              int64_t max_rows, int* status, cudaStream_t s)
 {
     const int64_t blocks = (c.T + 7) / 8;
-    router_bwd_kernel<<<(unsigned)blocks, 256, 0, s>>>(logits, ids, row_of, dw_row, counts, dlogits,
-                                                        c.T, c.E, c.K, c.score_func, c.renormalize,
+    router_bwd_kernel<<<(unsigned)blocks, 256, 0, s>>>(logits, ids, row_of, dw_row, counts, dlogits_add,
+                                                        dlogits, c.T, c.E, c.K, c.score_func, c.renormalize,
                                                         c.route_scale, c_bal, c_z, max_rows, status);
     return cudaGetLastError();
 }

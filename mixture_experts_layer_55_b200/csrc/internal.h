@@ -222,8 +222,8 @@ cudaError_t launch_bwd_rows(const moe_config& c, const void* dy, const void* o, 
                             int64_t max_rows, int* status, cudaStream_t s);
 cudaError_t launch_router_bwd(const moe_config& c, const float* logits, const int32_t* ids,
                               const int32_t* row_of, const float* dw_row, const int32_t* counts,
-                              float c_bal, float c_z, float* dlogits, int64_t max_rows, int* status,
-                              cudaStream_t s);
+                              float c_bal, float c_z, const float* dlogits_add, float* dlogits,
+                              int64_t max_rows, int* status, cudaStream_t s);
 int router_wgrad_splits(const moe_config& c);
 size_t router_wgrad_part_bytes(const moe_config& c, int splits);
 cudaError_t launch_router_wgrad(const moe_config& c, const void* x, const float* dL, float* part,
@@ -249,5 +249,28 @@ cudaError_t launch_permute_rows(const void* in, const int32_t* idx, void* out, i
 cudaError_t launch_dx_assemble(const moe_config& c, const float* dL, const float* w_r, const void* dxp,
                                const int32_t* row_of, const void* dx_shared, void* dx,
                                int64_t max_rows, cudaStream_t s);
+
+// ------------------------------------------------------- around the layer --
+cudaError_t launch_rmsnorm(int64_t T, int D, int dtype, const void* x, const void* residual, const float* gamma,
+                           float eps, void* s_out, void* n_out, float* rstd, void* q, void* scales,
+                           cudaStream_t s);
+size_t rmsnorm_backward_bytes(int64_t T, int D);
+cudaError_t launch_rmsnorm_backward(int64_t T, int D, int dtype, const void* dn, const void* ds, const void* s_in,
+                                    const float* gamma, const float* rstd, void* dx, float* dgamma, void* ws,
+                                    cudaStream_t s);
+cudaError_t launch_mx8_quantize(int64_t n, int dtype, const void* x, void* q, void* scales, cudaStream_t s);
+cudaError_t launch_mx8_dequantize(int64_t n, int dtype, const void* q, const void* scales, void* out,
+                                  cudaStream_t s);
+cudaError_t launch_mx8_weight(int E, int K, int N, int dtype, const void* w, void* q, void* scales, cudaStream_t s);
+cudaError_t launch_mx8_gather(const moe_config& c, const void* xq, const void* xs, const int32_t* offsets,
+                              const int32_t* perm, void* xq_perm, void* xs_perm, int64_t max_rows, int* status,
+                              cudaStream_t s);
+cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq, const void* xs,
+                           const int32_t* offsets, const int32_t* perm, const float* topk_w,
+                           const moe_mx8_weights& w, void* hq, void* hs, void* y_perm, int* status, cudaStream_t s);
+size_t balance_bytes(const moe_config& c, int64_t S);
+cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, const int32_t* ids,
+                           const int32_t* starts, const uint8_t* mask, float c_balance, float c_z, int32_t* counts,
+                           float* losses, float* seq_loss, float* dlogits, void* ws, cudaStream_t s);
 
 }  // namespace moe

@@ -21,12 +21,17 @@ class MoELayer:
     """
 
     def __init__(self, T: int, w_router, w_gate, w_up, w_down, K: int, capacity_factor=0.0,
-                 router_bias=None, selection_bias=None, shared=None, **router_options):
+                 router_bias=None, selection_bias=None, shared=None, experts=None, norm_weight=None,
+                 norm_eps: float = 1e-6, **router_options):
         """router_options: score_func ("softmax" | "sigmoid"), renormalize,
         n_groups, topk_groups, route_scale (see moe_config in include/moe.h).
         selection_bias (E) fp32: DeepSeek-V3 bias, for selection only.
         shared: (w_gate_s (D, Fs), w_up_s (D, Fs), w_down_s (Fs, D)), a shared
-        expert every token passes through."""
+        expert every token passes through.
+        experts: None, or "mx8": inference reads the expert weights in 8 bits
+        (moe_mx8_prepare_weight; quantize_experts() again after they change).
+        norm_weight (D) fp32, norm_eps: the norm of forward_block and
+        forward_block_train."""
         E, D, F = w_gate.shape
         dtype = "bf16" if w_gate.dtype == torch.bfloat16 else "f32"
         fs = 0 if shared is None else shared[0].shape[1]
@@ -52,6 +57,30 @@ class MoELayer:
         nb = B.router_terms_size(self.cfg)
         self.router_terms = torch.empty(nb, dtype=torch.uint8, device=self.device) if nb else None
         self._terms_of = None
+        self.norm_weight, self.norm_eps = norm_weight, norm_eps
+        if experts not in (None, "mx8"):
+            raise ValueError('experts: None or "mx8"')
+        self.mx8 = None
+        if experts == "mx8":
+            if shared is not None:
+                raise ValueError("8-bit experts: a shared expert is not supported")
+            nbytes = B.forward_mx8_workspace_size(self.cfg)
+            if nbytes > self.workspace.numel():
+                self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            self.quantize_experts()
+
+    def quantize_experts(self, stream=None):
+        """The expert weights into the 8-bit layout the layer's inference reads; call
+        it again whenever the weights have changed."""
+        if self.mx8 is None:
+            out = []
+            for w in (self.w_gate, self.w_up, self.w_down):
+                E, k, n = w.shape
+                out.append(torch.empty(E, n, k, dtype=torch.float8_e4m3fn, device=self.device))
+                out.append(torch.empty(E, n, k // 32, dtype=torch.uint8, device=self.device))
+            self.mx8 = tuple(out)
+        for i, w in enumerate((self.w_gate, self.w_up, self.w_down)):
+            B.moe_mx8_prepare_weight(w, self.mx8[2 * i], self.mx8[2 * i + 1], stream=stream)
 
     def _terms(self, stream=None):
         if self.router_terms is None:
@@ -68,6 +97,8 @@ class MoELayer:
         self.losses, self.mean_prob and self.counts."""
         if y is None:
             y = torch.empty_like(x)
+        if self.mx8 is not None:
+            return self._forward_mx8(x, y, logit_noise, stats, stream)
         B.moe_forward(self.cfg, x, self.w_router, self.w_gate, self.w_up, self.w_down, y,
                       self.workspace, w_router_terms=self._terms(stream),
                       router_bias=self.router_bias, logit_noise=logit_noise,
@@ -76,6 +107,41 @@ class MoELayer:
                       mean_prob=self.mean_prob if stats else None,
                       counts=self.counts if stats else None, stream=stream)
         return y
+
+    def _forward_mx8(self, x, y, logit_noise=None, stats=True, stream=None, xq=None, xs=None):
+        B.moe_forward_mx8(self.cfg, x, self.w_router, self.mx8, y, self.workspace, xq=xq, xs=xs,
+                          w_router_terms=self._terms(stream), router_bias=self.router_bias,
+                          logit_noise=logit_noise, selection_bias=self.selection_bias,
+                          losses=self.losses if stats else None,
+                          mean_prob=self.mean_prob if stats else None,
+                          counts=self.counts if stats else None, stream=stream)
+        return y
+
+    def _norm(self, x, residual, bits8=False, keep=False):
+        """moe_rmsnorm into new buffers: (n, s, q, q_scales, rstd)."""
+        if self.norm_weight is None:
+            raise ValueError("the layer has no norm_weight")
+        n = torch.empty_like(x)
+        s = torch.empty_like(x) if residual is not None else None
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if bits8 else None
+        qs = torch.empty(x.shape[0], x.shape[1] // 32, dtype=torch.uint8, device=x.device) if bits8 else None
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device) if keep else None
+        B.moe_rmsnorm(x, self.norm_weight, n, residual=residual, s=s, rstd=rstd, q=q, q_scales=qs,
+                      eps=self.norm_eps)
+        return n, x if s is None else s, q, qs, rstd
+
+    def forward_block(self, x, residual=None, y=None, logit_noise=None, stats: bool = True):
+        """The pre-norm block: s = x + residual, y = MoE(norm(s)); returns (y, s),
+        which the next block takes as its x and residual.  With 8-bit experts
+        the norm writes the rows they read.  On the current stream."""
+        n, s, q, qs, _ = self._norm(x, residual, bits8=self.mx8 is not None)
+        if y is None:
+            y = torch.empty_like(x)
+        if self.mx8 is not None:
+            self._forward_mx8(n, y, logit_noise, stats, xq=q, xs=qs)
+        else:
+            self.forward(n, y, logit_noise=logit_noise, stats=stats)
+        return y, s
 
     def capture(self, x, y, logit_noise=None, stats: bool = True):
         """One forward over the buffers x -> y captured as a CUDA graph; returns
@@ -158,6 +224,8 @@ class MoELayer:
     def forward_train(self, x, y=None, logit_noise=None, stream=None):
         """forward() that keeps the activations moe_backward reads; the state
         buffer is allocated on first use."""
+        if self.mx8 is not None:
+            raise ValueError("8-bit experts are for inference: train a layer without them")
         if getattr(self, "state", None) is None:
             self.state = torch.zeros(B.train_state_size(self.cfg), dtype=torch.uint8,
                                      device=self.device)
@@ -169,11 +237,60 @@ class MoELayer:
                             losses=self.losses, mean_prob=self.mean_prob, counts=self.counts,
                             stream=stream)
         self._train_x = x
+        self._block = None  # set again by forward_block_train
         return y
 
-    def backward(self, dy, c_balance: float = 0.0, c_z: float = 0.0, grads=None, stream=None):
+    def forward_block_train(self, x, residual=None, y=None, logit_noise=None):
+        """forward_block() that keeps what backward_block() reads; returns (y, s)."""
+        if self.mx8 is not None:
+            raise ValueError("8-bit experts are for inference: train a layer without them")
+        n, s, _, _, rstd = self._norm(x, residual, keep=True)
+        y = self.forward_train(n, y, logit_noise=logit_noise)
+        self._block = (s, rstd)
+        return y, s
+
+    def backward_block(self, dy, ds=None, c_balance: float = 0.0, c_z: float = 0.0, grads=None,
+                       dlogits_add=None):
+        """backward() of the last forward_block_train, through its norm: ds is the
+        gradient that arrives at s (None: none), dx the gradient of x and of the
+        residual alike, dgamma (D) fp32 the norm weight's."""
+        if getattr(self, "_block", None) is None:
+            raise RuntimeError("backward_block() needs a forward_block_train() first")
+        s, rstd = self._block
+        grads = self.backward(dy, c_balance, c_z, grads, dlogits_add=dlogits_add)
+        if "dgamma" not in grads:
+            grads["dgamma"] = torch.empty(s.shape[1], dtype=torch.float32, device=s.device)
+        if getattr(self, "norm_workspace", None) is None:
+            self.norm_workspace = torch.zeros(B.rmsnorm_backward_workspace_size(*s.shape), dtype=torch.uint8,
+                                              device=s.device)
+        B.moe_rmsnorm_backward(grads["dx"], s, self.norm_weight, rstd, grads["dx"], grads["dgamma"],
+                               self.norm_workspace, ds=ds)
+        return grads
+
+    def balance_loss(self, seq_starts, token_mask=None, c_balance: float = 0.0, c_z: float = 0.0):
+        """moe_balance_loss of the last forward_train's routing over the sequences
+        seq_starts (S + 1) int32 and the tokens of token_mask: a dict of losses
+        [z, balance], seq_loss (S), counts (S, E) and dlogits (T, E), the gradient
+        of c_balance * balance + c_z * z that backward() adds as dlogits_add.  On the
+        current stream."""
+        if getattr(self, "_train_x", None) is None:
+            raise RuntimeError("balance_loss() needs a forward_train() first")
+        T, E, K, S = self.cfg.T, self.cfg.E, self.cfg.K, seq_starts.numel() - 1
+        lo, io = B.train_state_router(self.cfg)
+        logits = self.state[lo:lo + 4 * T * E].view(torch.float32)
+        ids = self.state[io:io + 4 * T * K].view(torch.int32)
+        f32 = dict(dtype=torch.float32, device=self.device)
+        ws = torch.zeros(B.balance_workspace_size(self.cfg, S), dtype=torch.uint8, device=self.device)
+        out = dict(losses=torch.empty(2, **f32), seq_loss=torch.empty(S, **f32), dlogits=torch.empty(T, E, **f32),
+                   counts=torch.empty(S, E, dtype=torch.int32, device=self.device))
+        B.moe_balance_loss(self.cfg, logits, ids, seq_starts, out["counts"], out["losses"], out["seq_loss"], ws,
+                           token_mask=token_mask, dlogits=out["dlogits"], c_balance=c_balance, c_z=c_z)
+        return out
+
+    def backward(self, dy, c_balance: float = 0.0, c_z: float = 0.0, grads=None, stream=None, dlogits_add=None):
         """Gradients of sum(dy * y) + c_balance * balance + c_z * z for the
-        last forward_train.  Returns a dict of dx (layer dtype) and fp32
+        last forward_train; dlogits_add (T, E) fp32, a further gradient of the
+        routing logits (balance_loss()'s), is added to theirs.  Returns a dict of dx (layer dtype) and fp32
         dw_router, db_router (when the layer has a router bias), dw_gate,
         dw_up, dw_down (and dshared); ``grads`` may pass that dict back to
         reuse its buffers."""
@@ -198,7 +315,7 @@ class MoELayer:
                        dy, grads["dx"], grads["dw_router"], grads["dw_gate"], grads["dw_up"],
                        grads["dw_down"], self.bwd_workspace, c_balance=c_balance, c_z=c_z,
                        db_router=grads.get("db_router"), shared=self.shared,
-                       dshared=grads.get("dshared"), stream=stream)
+                       dshared=grads.get("dshared"), stream=stream, dlogits_add=dlogits_add)
         return grads
 
     def update_selection_bias(self, gamma: float, stream=None):
