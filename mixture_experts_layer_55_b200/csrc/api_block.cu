@@ -194,7 +194,8 @@ moe_status moe_expert_ffn_mx8(const moe_config* cfg, const void* xq, const void*
     st = check_scratch(workspace, workspace_bytes, mx8_ws_bytes(*cfg));
     if (st != MOE_OK) return st;
     return cuda_status(launch_ffn_mx8(*cfg, max_rows_of(*cfg), xq, xs, offsets, perm, topk_w, *weights, hq, hs,
-                                      y_perm, static_cast<int*>(workspace), static_cast<cudaStream_t>(stream)));
+                                      y_perm, static_cast<char*>(workspace) + align_up(64 * sizeof(int)),
+                                      static_cast<int*>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_forward_mx8_workspace_size(const moe_config* cfg, size_t* bytes)
@@ -250,7 +251,7 @@ moe_status moe_forward_mx8(const moe_config* cfg, const void* x, const void* xq,
         e = launch_mx8_gather(c, xq, xs, offsets, perm, ws + F.xq_perm, ws + F.xs_perm, max_rows, status, s);
     if (e == cudaSuccess)
         e = launch_ffn_mx8(c, max_rows, ws + F.xq_perm, ws + F.xs_perm, offsets, perm, w, *weights, ws + F.hq,
-                           ws + F.hs, ws + F.y_perm, status, s);
+                           ws + F.hs, ws + F.y_perm, ws + F.amaps, status, s);
     if (e == cudaSuccess) e = launch_combine(c, ws + F.y_perm, row_of, nullptr, y_add, y, max_rows, s);
     return cuda_status(e);
 }

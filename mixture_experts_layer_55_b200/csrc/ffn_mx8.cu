@@ -1,127 +1,755 @@
-// ffn_mx8.cu -- grouped SwiGLU experts on 8-bit rows and weights.
+// ffn_mx8.cu -- grouped SwiGLU experts on 8-bit rows and weights, on the tensor
+// cores' block-scaled MMA (tcgen05, kind::mxf8f6f4).
 //
 // Rows and weights are e4m3 in blocks of 32 along the contracted axis with
 // power-of-two scales (mx8.cuh); for every row r of expert e
 //   g = x_r . Wg_e,  u = x_r . Wu_e                       (K = D, fp32 sums)
 //   h_r = 8-bit blocks of silu(g) u                       (blocks of 32 along F)
 //   y_r = bf16(w_r (h_r . Wd_e))                          (K = F)
-// h is rounded to 8 bits straight from fp32: at most 2^-4 of a value, the
-// precision of every operand of these products.
+// h is rounded to 8 bits straight from the fp32 accumulators: at most 2^-4 of a
+// value, the precision of every operand of these products.
 //
-// A simple kernel: 64 rows by 32 columns per block, the operands' values in
-// shared memory in fp32, 32 of the contracted axis at a time.
+// Persistent kernel on the tiles of the bf16 experts (ffn_tc.cu): 128 rows per
+// CTA, or 256 per CTA pair (cta_group::2), by 256 accumulator columns (gate/up:
+// 128 of F, gate and up interleaved in blocks of 64; down: 256 of D).  A stage
+// is 128 of the contracted axis: one 128-byte swizzle row of A and of B (both
+// K-major), four MMAs of K = 32, each with one scale per row.  14 warps per CTA:
+//   warp 0       TMA producer: A 128 x 128 and B 256 (pair: 128) x 128 bytes
+//   warp 1       MMA issuer (pair: the leader's); owns the tensor memory
+//   warps 2..5   scales: a thread per row of A and two of B loads the scales of
+//                four stages at once (16 bytes of a row where rows allow it),
+//                one such group ahead, and writes each stage's as 32 x 16-byte
+//                blocks [row % 32][row / 32][4 of K]; tcgen05.cp replicates them
+//                over the four lane quadrants of tensor memory
+//   warps 6..13  epilogue: two per lane quadrant, each half of the columns
+// Tensor memory: two accumulators of 256 columns and the scales do not fit 512
+// columns, so the accumulators overlap by 32 (0..255 and 224..479, scales from
+// 480).  The epilogue empties the shared columns first and says so; the next
+// tile's MMAs start then, not when the whole accumulator has been read.
+#include <cuda.h>
+
 #include "internal.h"
 #include "mx8.cuh"
 
 namespace moe {
 
-constexpr int kSM = 64, kSN = 32;
+// ffn_tc.cu: the per-expert A maps (row extent cut to the expert's end)
+cudaError_t launch_ffn_amaps(const void* map_x, const void* map_h, const int32_t* offsets, int E, int64_t max_rows,
+                             void* maps, cudaStream_t s);
 
-struct Mx8Args {
+namespace mx {
+
+constexpr int BK = 128;                // contracted elements (bytes) per stage
+constexpr int A_BYTES = 128 * BK;
+constexpr int SF_BYTES = 3 * 512;      // scales of 128 rows of A and 256 of B, 4 per row
+constexpr int ACC_STRIDE = 224;        // second accumulator's first column
+constexpr int SF_COL = 480;            // A's scales: 4 columns, then B's 8
+constexpr int TMEM_COLS = 512;
+constexpr int SF_WARPS = 4;
+constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARP0 = 2 + SF_WARPS;
+constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int OUT_BYTES = 2048;        // an epilogue warp's 32 x 32 bf16 piece (down)
+constexpr int MAX_E = 256;
+
+template <bool PAIR> struct Geo {
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int BM = 128 * CTAS;
+    static constexpr int B_ROWS = 256 / CTAS;              // rows of B in this CTA
+    static constexpr int B_BYTES = B_ROWS * BK;
+    static constexpr int OP_BYTES = A_BYTES + B_BYTES;     // one stage's operands
+    static constexpr int STAGES = PAIR ? 6 : 4;
+};
+
+struct Misc {
+    uint64_t full[8];
+    uint64_t sfull[8];    // the stage's scales are in shared memory (both CTAs')
+    uint64_t empty[8];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t tover;       // the accumulators' shared columns have been read
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int row0[MAX_E];
+    int rowend[MAX_E];
+    int pref[MAX_E + 1];
+};
+
+template <bool PAIR> constexpr size_t smem_bytes()
+{
+    return 1024 + (size_t)Geo<PAIR>::STAGES * (Geo<PAIR>::OP_BYTES + SF_BYTES) + EPI_WARPS * OUT_BYTES + sizeof(Misc);
+}
+
+struct Args {
     const int32_t* offsets;
     const int32_t* perm;
     const float* topk_w;
-    const uint8_t *a, *as;    // (rows, Kdim), (rows, Kdim / 32)
-    const uint8_t *b0, *b0s;  // (E, N, Kdim), (E, N, Kdim / 32): gate, or down
-    const uint8_t *b1, *b1s;  // up
-    uint8_t *h, *hs;          // gate/up: (rows, N), (rows, N / 32)
-    __nv_bfloat16* y;         // down: (rows, N)
-    int E, N, Kdim;
+    const uint8_t* as;         // A's scales (rows, Kdim / 32)
+    const uint8_t *b0s, *b1s;  // B's scales (E, N, Kdim / 32): gate or down; up
+    uint8_t *h, *hs;           // gate/up's output
+    __nv_bfloat16* y;          // down's
+    int E, Kdim, N, n_tiles;
     int64_t max_rows, nk;
     int* status;
+    const CUtensorMap* amaps;  // A's map per expert (null: tmA)
 };
 
-template <bool GATEUP> __global__ void __launch_bounds__(256) ffn_mx8_simple_kernel(Mx8Args a)
+// ------------------------------------------------------------------- PTX --
+// Instruction descriptor of kind::mxf8f6f4: e4m3 operands (format 0), scales of
+// type UE8M0 (bit 23); bits 4-5 and 29-30 pick the scale byte of B and of A.
+MOE_DEVICE constexpr uint32_t mx_idesc(int M, int N)
 {
-    __shared__ float sa[kSM][33], sb[GATEUP ? 2 : 1][kSN][33];
-    // the expert and rows of this block's tile
-    int e = 0, r0 = 0, r1 = 0;
-    int64_t m = blockIdx.y;
-    for (; e < a.E; ++e) {
-        r0 = a.offsets[e];
-        r1 = a.offsets[e + 1];
-        if (r0 < 0 || r1 < r0 || r1 > a.max_rows) {
-            if (threadIdx.x == 0) raise_flag(a.status, kFlagBounds, 720);
-            return;
-        }
-        const int64_t tiles = (r1 - r0 + kSM - 1) / kSM;
-        if (m < tiles) break;
-        m -= tiles;
+    return (1u << 23) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+template <bool PAIR>
+MOE_DEVICE void mma_mx8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                        uint32_t accumulate)
+{
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// 32 x 16 bytes of shared memory to four columns, replicated over the lane
+// quadrants (pair: in both CTAs, each from its own shared memory).
+template <bool PAIR> MOE_DEVICE void copy_scales(uint32_t taddr, uint64_t desc)
+{
+    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Descriptor of a block of scales: no swizzle, groups of 8 rows 128 bytes apart.
+MOE_DEVICE uint64_t scale_desc(uint32_t smem_addr)
+{
+    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1u << 46);
+}
+
+// ----------------------------------------------------------------- tiles --
+MOE_DEVICE void decode_tile(const Misc* m, int E, int bm, int bn, int t, int& e, int& m_row0, int& row_end, int& n0)
+{
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {  // largest e with pref[e] <= t (its block is non-empty)
+        const int mid = (lo + hi + 1) >> 1;
+        if (m->pref[mid] <= t) lo = mid;
+        else hi = mid - 1;
     }
-    if (e == a.E) return;
-    r0 += (int)m * kSM;
-    const int n0 = blockIdx.x * kSN;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;  // column, group of 8 rows
-    const int nb = a.Kdim / kMxBlock;
-    float c0[8], c1[8];
-    for (int i = 0; i < 8; ++i) c0[i] = c1[i] = 0.f;
-    for (int kb = 0; kb < nb; ++kb) {
-        for (int i = 0; i < 8; ++i) {
-            const int r = r0 + ty * 8 + i;
-            sa[ty * 8 + i][tx] =
-                r < r1 ? e4m3_to_f32(a.a[(int64_t)r * a.Kdim + kb * 32 + tx]) * mx_scale(a.as[(int64_t)r * nb + kb])
-                       : 0.f;
+    e = lo;
+    const int mt = (m->rowend[e] - m->row0[e] + bm - 1) / bm;
+    const int local = t - m->pref[e];
+    const int n = local / mt, mm = local - n * mt;
+    m_row0 = m->row0[e] + mm * bm;
+    row_end = m->rowend[e];
+    n0 = n * bn;
+}
+
+// Scales of stages 4g .. 4g+3 of one row (null: zeros), nb = bytes per row.
+// Rows are 16-byte, 4-byte or only byte aligned with nb.
+MOE_DEVICE uint4 load_scales(const uint8_t* row, int g, int nb)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row == nullptr) return v;
+    if ((nb & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(row) + g);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = 16 * g + 4 * i;
+        w[i] = 0;
+        if ((nb & 3) == 0) {
+            if (at < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + at));
+        } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (at + b < nb) w[i] |= (uint32_t)__ldg(row + at + b) << (8 * b);
         }
-        for (int i = 0; i < 4; ++i) {
-            const int n = n0 + ty * 4 + i;
-            const int64_t row = (int64_t)e * a.N + n;
-            sb[0][ty * 4 + i][tx] =
-                n < a.N ? e4m3_to_f32(a.b0[row * a.Kdim + kb * 32 + tx]) * mx_scale(a.b0s[row * nb + kb]) : 0.f;
-            if (GATEUP)
-                sb[GATEUP ? 1 : 0][ty * 4 + i][tx] =
-                    n < a.N ? e4m3_to_f32(a.b1[row * a.Kdim + kb * 32 + tx]) * mx_scale(a.b1s[row * nb + kb]) : 0.f;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+MOE_DEVICE uint32_t word_of(const uint4& v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// silu(g) u in fp32: the exponential and the quotient to 2^-21, so that the one
+// rounding of h is the 8-bit one.
+MOE_DEVICE float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+template <bool GATEUP, bool PAIR>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    ffn_mx8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
+                   const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmY, const Args a)
+{
+    using G = Geo<PAIR>;
+    constexpr int BM = G::BM, BN = GATEUP ? 128 : 256, STAGES = G::STAGES, OP_BYTES = G::OP_BYTES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* stages = smem;
+    uint8_t* outbuf = smem + (size_t)STAGES * OP_BYTES;
+    uint8_t* scales = outbuf + (size_t)EPI_WARPS * OUT_BYTES;
+    Misc* m = reinterpret_cast<Misc*>(scales + (size_t)STAGES * SF_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = a.E;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;  // 0: the leader, which issues the MMAs
+    const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int units = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&m->full[s], 1);
+            mbar_init(&m->sfull[s], SF_WARPS * G::CTAS);
+            mbar_init(&m->empty[s], 1);
         }
-        __syncthreads();
-        for (int k = 0; k < 32; ++k)
-            for (int i = 0; i < 8; ++i) {
-                c0[i] = fmaf(sa[ty * 8 + i][k], sb[0][tx][k], c0[i]);
-                if (GATEUP) c1[i] = fmaf(sa[ty * 8 + i][k], sb[GATEUP ? 1 : 0][tx][k], c1[i]);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&m->tfull[b], 1);
+            mbar_init(&m->tempty[b], EPI_WARPS * G::CTAS);
+        }
+        mbar_init(&m->tover, EPI_WARPS / 2 * G::CTAS);
+        mbar_init(&m->drain, 1);
+        m->abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB0);
+        if (GATEUP) prefetch_tmap(&tmB1);
+        else prefetch_tmap(&tmY);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            tmem_alloc_pair(&m->tmem_base, TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&m->tmem_base, TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    // tile table from the offsets (a malformed block is treated as empty)
+    for (int e = threadIdx.x; e < E; e += NUM_THREADS) {
+        m->row0[e] = a.offsets[e];
+        m->rowend[e] = a.offsets[e + 1];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int run = 0, prev = 0;
+        for (int e = 0; e < E; ++e) {
+            int r0 = m->row0[e], r1 = m->rowend[e];
+            if (r0 < prev || r1 < r0 || (int64_t)r1 > a.max_rows) {
+                raise_flag(a.status, kFlagBounds, 720);
+                r0 = r1 = prev;
             }
-        __syncthreads();
+            m->row0[e] = r0;
+            m->rowend[e] = r1;
+            prev = r1;
+            m->pref[e] = run;
+            run += (r1 - r0 + BM - 1) / BM * a.n_tiles;
+        }
+        m->pref[E] = run;
     }
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + ty * 8 + i;  // uniform in the warp
-        if (r >= r1) break;
-        if (GATEUP) {
-            const float h = silu_f32(c0[i]) * c1[i];
-            const uint32_t mx = __reduce_max_sync(0xffffffffu, abs_bits(h));
-            const uint32_t b = mx_scale_byte(mx);
-            a.h[(int64_t)r * a.N + n0 + tx] = (uint8_t)(mx_pack4(h, 0.f, 0.f, 0.f, mx_inv_scale(b)) & 0xffu);
-            if (tx == 0) a.hs[(int64_t)r * (a.N / 32) + n0 / 32] = (uint8_t)b;
-        } else if (n0 + tx < a.N) {
+    tc_fence_before();
+    if (PAIR) cluster_sync();  // the peer's barriers are initialised before any remote signal
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = m->tmem_base;
+    const int total = m->pref[E];
+    const int num_kb = (a.Kdim + BK - 1) / BK;
+    volatile int* abort_flag = &m->abort_flag;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer (each CTA)
+            int stage = 0;
+            uint32_t phase = 0;
+            int last_phase[STAGES];
+            for (int s = 0; s < STAGES; ++s) last_phase[s] = -1;
+            bool ok = true;
+            int last_e = -1;
+            for (int t = unit; t < total && ok; t += units) {
+                int e, m_row0, row_end, n0;
+                decode_tile(m, E, BM, BN, t, e, m_row0, row_end, n0);
+                const int a_row = m_row0 + (int)rank * 128;
+                const CUtensorMap* mA = &tmA;
+                if (a.amaps != nullptr) {  // the expert's own map: rows past its end read as zeros
+                    mA = a.amaps + e;
+                    if (e != last_e) {
+                        asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mA) : "memory");
+                        last_e = e;
+                    }
+                }
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait(&m->empty[stage], phase ^ 1u, a.status, 722, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sA = stages + (size_t)stage * OP_BYTES;
+                    uint8_t* sB = sA + A_BYTES;
+                    const int k0 = kb * BK;
+                    if (PAIR) {
+                        // both CTAs' bytes are counted on the leader's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(&m->full[stage], 2 * OP_BYTES);
+                        const uint32_t fb = mapa_shared(smem_u32(&m->full[stage]), 0);
+                        tma_load_2d_pair(sA, mA, k0, a_row, fb);
+                        if (GATEUP) {  // this CTA's [gate 64 | up 64]
+                            tma_load_3d_pair(sB, &tmB0, k0, n0 + 64 * (int)rank, e, fb);
+                            tma_load_3d_pair(sB + 64 * BK, &tmB1, k0, n0 + 64 * (int)rank, e, fb);
+                        } else {
+                            tma_load_3d_pair(sB, &tmB0, k0, n0 + 128 * (int)rank, e, fb);
+                            tma_load_3d_pair(sB + 64 * BK, &tmB0, k0, n0 + 128 * (int)rank + 64, e, fb);
+                        }
+                    } else {
+                        uint64_t* fb = &m->full[stage];
+                        mbar_arrive_expect_tx(fb, OP_BYTES);
+                        tma_load_2d(sA, mA, k0, a_row, fb);
+                        if (GATEUP) {  // [gate | up | gate | up], 64 each
+                            tma_load_3d(sB, &tmB0, k0, n0, e, fb);
+                            tma_load_3d(sB + 64 * BK, &tmB1, k0, n0, e, fb);
+                            tma_load_3d(sB + 128 * BK, &tmB0, k0, n0 + 64, e, fb);
+                            tma_load_3d(sB + 192 * BK, &tmB1, k0, n0 + 64, e, fb);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tma_load_3d(sB + 64 * j * BK, &tmB0, k0, n0 + 64 * j, e, fb);
+                        }
+                    }
+                    last_phase[stage] = (int)phase;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // never leave the CTA with a copy in flight (the leader sees every completion)
+            if (!PAIR || rank == 0)
+                for (int s = 0; s < STAGES; ++s)
+                    if (last_phase[s] >= 0) mbar_wait(&m->full[s], (uint32_t)last_phase[s], a.status, 723, nullptr);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------ MMA issuer (leader only)
+            constexpr uint32_t idesc = mx_idesc(BM, 256);
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0, over_phase = 1;  // no tile before the first one
+            bool ok = true;
+            for (int t = unit; t < total && ok; t += units) {
+                // this accumulator's last tile has been read, and the shared
+                // columns of the tile before this one
+                if (!mbar_wait(&m->tempty[acc], acc_phase ^ 1u, a.status, 724, abort_flag)) break;
+                if (!mbar_wait(&m->tover, over_phase, a.status, 725, abort_flag)) break;
+                over_phase ^= 1u;
+                tc_fence_after();
+                const uint32_t d0 = tmem_base + (uint32_t)(acc * ACC_STRIDE);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait(&m->full[stage], phase, a.status, 726, abort_flag) ||
+                        !mbar_wait(&m->sfull[stage], phase, a.status, 727, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sA = smem_u32(stages + (size_t)stage * OP_BYTES);
+                    const uint32_t sB = sA + A_BYTES;
+                    const uint32_t sS = smem_u32(scales + (size_t)stage * SF_BYTES);
+                    // the copies and the MMAs of one thread run in order
+                    const uint32_t tsa = tmem_base + SF_COL, tsb = tsa + 4;
+                    copy_scales<PAIR>(tsa, scale_desc(sS));
+                    copy_scales<PAIR>(tsb, scale_desc(sS + 512));
+                    copy_scales<PAIR>(tsb + 4, scale_desc(sS + 1024));
+#pragma unroll
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        mma_mx8<PAIR>(d0, umma_desc_sw128(sA + kk * 32, 16, 1024), umma_desc_sw128(sB + kk * 32, 16, 1024),
+                                      idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), tsa, tsb,
+                                      (kb | kk) != 0 ? 1u : 0u);
+                    // frees the stage (in both CTAs) once these complete
+                    if (PAIR) umma_commit_pair_mc(&m->empty[stage], 0x3);
+                    else umma_commit(&m->empty[stage]);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (PAIR) umma_commit_pair_mc(&m->tfull[acc], 0x3);
+                else umma_commit(&m->tfull[acc]);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            // every MMA issued here is done before the allocation is released
+            if (PAIR) umma_commit_pair_mc(&m->drain, 0x1);
+            else umma_commit(&m->drain);
+            mbar_wait(&m->drain, 0, a.status, 728, nullptr);
+        }
+    } else if (warp < EPI_WARP0) {
+        // ------------------------------------------------ scales (each CTA: its A rows, all of B's)
+        const int i = (warp - 2) * 32 + lane;
+        const int nb = a.Kdim / kMxBlock, groups = (num_kb + 3) / 4;
+        const uint32_t off = (uint32_t)((i & 31) * 16 + (i >> 5) * 4);
+        const uint8_t *pa = nullptr, *pb0 = nullptr, *pb1 = nullptr;
+        auto rows_of = [&](int t) {
+            int e, m_row0, row_end, n0;
+            decode_tile(m, E, BM, BN, t, e, m_row0, row_end, n0);
+            const int64_t row = (int64_t)m_row0 + (int)rank * 128 + i;
+            pa = row < row_end ? a.as + row * nb : nullptr;
+            // accumulator columns i and 128 + i: gate/up blocks of 64, or down
+            const uint8_t* bs = GATEUP && i >= 64 ? a.b1s : a.b0s;
+            const int n = GATEUP ? n0 + (i & 63) : n0 + i;
+            const int n2 = GATEUP ? n + 64 : n + 128;
+            const int64_t be = (int64_t)e * a.N;
+            pb0 = n < a.N ? bs + (be + n) * nb : nullptr;
+            pb1 = n2 < a.N ? bs + (be + n2) * nb : nullptr;
+        };
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        uint4 va = make_uint4(0, 0, 0, 0), v0 = va, v1 = va;
+        if (unit < total) {
+            rows_of(unit);
+            va = load_scales(pa, 0, nb);
+            v0 = load_scales(pb0, 0, nb);
+            v1 = load_scales(pb1, 0, nb);
+        }
+        for (int t = unit; t < total && ok; t += units) {
+            for (int g = 0; g < groups && ok; ++g) {
+                // the next group's loads, of this tile or of the next one
+                uint4 na = make_uint4(0, 0, 0, 0), n0v = na, n1v = na;
+                int ng = g + 1;
+                bool more = true;
+                if (ng == groups) {
+                    ng = 0;
+                    more = t + units < total;
+                    if (more) rows_of(t + units);
+                }
+                if (more) {
+                    na = load_scales(pa, ng, nb);
+                    n0v = load_scales(pb0, ng, nb);
+                    n1v = load_scales(pb1, ng, nb);
+                }
+                const int kbs = num_kb - 4 * g < 4 ? num_kb - 4 * g : 4;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k >= kbs) break;
+                    if (!__all_sync(0xffffffffu, mbar_wait(&m->empty[stage], phase ^ 1u, a.status, 729, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = scales + (size_t)stage * SF_BYTES + off;
+                    *reinterpret_cast<uint32_t*>(dst) = word_of(va, k);
+                    *reinterpret_cast<uint32_t*>(dst + 512) = word_of(v0, k);
+                    *reinterpret_cast<uint32_t*>(dst + 1024) = word_of(v1, k);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&m->sfull[stage]), 0));
+                        else mbar_arrive(&m->sfull[stage]);
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                va = na;
+                v0 = n0v;
+                v1 = n1v;
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue (each CTA, its 128 rows)
+        const int quad = warp & 3;
+        const int half = (warp - EPI_WARP0) >> 2;
+        const int r_in_tile = (int)rank * 128 + quad * 32 + lane;
+        const uint32_t tempty0 = mapa_shared(smem_u32(&m->tempty[0]), 0);
+        const uint32_t tempty1 = mapa_shared(smem_u32(&m->tempty[1]), 0);
+        const uint32_t tover = mapa_shared(smem_u32(&m->tover), 0);
+        uint8_t* obuf = outbuf + (size_t)(warp - EPI_WARP0) * OUT_BYTES;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int t = unit; t < total; t += units) {
+            int e, m_row0, row_end, n0;
+            decode_tile(m, E, BM, BN, t, e, m_row0, row_end, n0);
+            if (!__all_sync(0xffffffffu, mbar_wait(&m->tfull[acc], acc_phase, a.status, 730, abort_flag))) break;
+            tc_fence_after();
+            const int64_t row = (int64_t)m_row0 + r_in_tile;
+            const bool valid = row < row_end;
+            const int64_t warp_row0 = (int64_t)m_row0 + (int)rank * 128 + quad * 32;
+            const bool warp_full = warp_row0 + 32 <= row_end;
+            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * ACC_STRIDE);
+            // the shared columns: the last 32 of accumulator 0, the first 32 of 1
+            const bool shared_half = half == (acc == 0 ? 1 : 0);
             float w = 1.f;
-            if (a.perm != nullptr) {
-                const int32_t p = a.perm[r];
-                if (p >= 0 && (int64_t)p < a.nk) w = a.topk_w[p];
-                else { raise_flag(a.status, kFlagBounds, 721); w = 0.f; }
+            if (!GATEUP && valid && a.perm != nullptr) {
+                const int32_t pa = a.perm[row];
+                w = 0.f;
+                if (pa >= 0 && (int64_t)pa < a.nk) w = a.topk_w[pa];
+                else if (half == 0) raise_flag(a.status, kFlagBounds, 721);
             }
-            a.y[(int64_t)r * a.N + n0 + tx] = __float2bfloat16_rn(w * c0[i]);
+            constexpr int CHUNKS = GATEUP ? 2 : 4;
+#pragma unroll 1
+            for (int cc = 0; cc < CHUNKS; ++cc) {
+                const int c = half * CHUNKS + (acc == 0 ? CHUNKS - 1 - cc : cc);
+                const int col = n0 + c * 32;
+                uint32_t v[32], u[32];
+                if (GATEUP) {  // columns [gate 0-63 | up 0-63 | gate 64-127 | up 64-127]
+                    const uint32_t gcol = (uint32_t)((c >> 1) * 128 + (c & 1) * 32);
+                    tmem_ld_32x32b_x32(taddr + gcol, v);
+                    tmem_ld_32x32b_x32(taddr + gcol + 64, u);
+                } else {
+                    tmem_ld_32x32b_x32(taddr + c * 32, v);
+                }
+                tmem_ld_wait();
+                if (cc == 0 && shared_half) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(tover);
+                        else mbar_arrive(&m->tover);
+                    }
+                }
+                if (GATEUP) {
+                    if (valid && col < a.N) {
+                        uint32_t mx = 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float h = swiglu(__uint_as_float(v[j]), __uint_as_float(u[j]));
+                            v[j] = __float_as_uint(h);
+                            mx = max(mx, abs_bits(h));
+                        }
+                        const uint32_t b = mx_scale_byte(mx);
+                        const float inv = mx_inv_scale(b);
+                        uint32_t p[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            p[j] = mx_pack4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                            __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), inv);
+                        uint4* dst = reinterpret_cast<uint4*>(a.h + row * a.N + col);
+                        dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                        dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                        a.hs[row * (a.N / kMxBlock) + col / kMxBlock] = (uint8_t)b;
+                    }
+                } else if (col < a.N) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        p[j] = pack_bf16x2(w * __uint_as_float(v[2 * j]), w * __uint_as_float(v[2 * j + 1]));
+                    if (warp_full) {  // through shared memory (64-byte swizzle) and a TMA store
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                        uint4* dst = reinterpret_cast<uint4*>(obuf + lane * 64);
+                        const int sw = (lane >> 1) & 3;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dst[q ^ sw] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tmY, obuf, col, (int)warp_row0);
+                            bulk_commit();
+                        }
+                    } else if (valid) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.y + row * a.N + col);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dst[q] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(acc == 0 ? tempty0 : tempty1);
+                else mbar_arrive(&m->tempty[acc]);
+            }
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
         }
+        if (lane == 0) bulk_wait_all<0>();  // every store of this warp has completed
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (PAIR) cluster_sync();  // no CTA leaves while its peer may still signal it
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        if (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
 // ------------------------------------------------------------------- host --
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encoder()
+{
+    static std::atomic<EncodeTiledFn> cached{nullptr};
+    EncodeTiledFn fn = cached.load(std::memory_order_acquire);
+    if (fn == nullptr) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess) {
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+            cached.store(fn, std::memory_order_release);
+        }
+    }
+    return fn;
+}
+
+// Row-major bytes (.., rows, K), read in boxes of box_rows x 128 with the
+// 128-byte swizzle; E = 0: two dimensions.
+static bool map_bytes(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t E, uint32_t box_rows)
+{
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {K, rows, E};
+    cuuint64_t strides[2] = {K, K * rows};
+    cuuint32_t box[3] = {BK, box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, E ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y (rows, cols) bf16 for 32 x 32 stores from shared memory (64-byte swizzle)
+static bool map_store(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows)
+{
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols * 2};
+    cuuint32_t box[2] = {32, 32};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Per device: shared memory opted in, and how many CTAs or pairs are resident.
+template <bool GATEUP, bool PAIR> static cudaError_t prepare(int* resident)
+{
+    static std::atomic<int> cached[32];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 32) {
+        const int v = cached[dev].load(std::memory_order_acquire);
+        if (v > 0) {
+            *resident = v;
+            return cudaSuccess;
+        }
+    }
+    constexpr size_t smem = smem_bytes<PAIR>();
+    e = cudaFuncSetAttribute(ffn_mx8_kernel<GATEUP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    int units = 0;
+    if (PAIR) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2, 1, 1);
+        cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&units, ffn_mx8_kernel<GATEUP, PAIR>, &cfg);
+    } else {
+        e = cudaDeviceGetAttribute(&units, cudaDevAttrMultiProcessorCount, dev);  // one CTA per SM
+    }
+    if (e != cudaSuccess) return e;
+    if (units < 1) return cudaErrorInvalidConfiguration;
+    if (dev >= 0 && dev < 32) cached[dev].store(units, std::memory_order_release);
+    *resident = units;
+    return cudaSuccess;
+}
+
+template <bool GATEUP, bool PAIR>
+static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, const CUtensorMap& mB1,
+                              const CUtensorMap& mY, const Args& a, int64_t tiles_bound, cudaStream_t s)
+{
+    int units = 0;
+    cudaError_t e = prepare<GATEUP, PAIR>(&units);
+    if (e != cudaSuccess) return e;
+    int64_t n = tiles_bound < units ? tiles_bound : units;
+    if (n < 1) n = 1;
+    constexpr size_t smem = smem_bytes<PAIR>();
+    if (!PAIR) {
+        ffn_mx8_kernel<GATEUP, false><<<(unsigned)n, NUM_THREADS, smem, s>>>(mA, mB0, mB1, mY, a);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(2 * n), 1, 1);
+    cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, true>, mA, mB0, mB1, mY, a);
+}
+
+}  // namespace mx
+
 cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq, const void* xs,
                            const int32_t* offsets, const int32_t* perm, const float* topk_w,
-                           const moe_mx8_weights& w, void* hq, void* hs, void* y_perm, int* status, cudaStream_t s)
+                           const moe_mx8_weights& w, void* hq, void* hs, void* y_perm, void* amaps, int* status,
+                           cudaStream_t s)
 {
+    using namespace mx;
     auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
-    const unsigned mt = (unsigned)((max_rows + kSM - 1) / kSM + c.E);
-    Mx8Args a{};
+    const uint64_t D = (uint64_t)c.D, F = (uint64_t)c.F, E = (uint64_t)c.E, R = (uint64_t)max_rows;
+    CUtensorMap mX, mG, mU, mH, mD, mY;
+    if (!map_bytes(&mX, xq, D, R, 0, 128) || !map_bytes(&mG, w.gate, D, F, E, 64) ||
+        !map_bytes(&mU, w.up, D, F, E, 64) || !map_bytes(&mH, hq, F, R, 0, 128) ||
+        !map_bytes(&mD, w.down, F, D, E, 64) || !map_store(&mY, y_perm, D, R))
+        return cudaErrorInvalidValue;
+    // CTA pairs when experts hold 128 rows or more on average, as the bf16
+    // experts: single CTAs waste fewer padded rows on a few tokens each
+    const bool pair = max_rows >= 128 * (int64_t)c.E;
+    const int64_t bm = pair ? 256 : 128;
+    const int64_t mt = (max_rows + bm - 1) / bm + c.E;
+    // rows of a tile past its expert's end are not fetched: worth a launch only
+    // where a tile can reach other experts' rows beyond one tile of them all
+    const CUtensorMap* gm = nullptr;
+    if (max_rows > 128) {
+        cudaError_t e = launch_ffn_amaps(&mX, &mH, offsets, c.E, max_rows, amaps, s);
+        if (e != cudaSuccess) return e;
+        gm = static_cast<const CUtensorMap*>(amaps);
+    }
+    Args a{};
     a.offsets = offsets; a.perm = perm; a.topk_w = topk_w;
-    a.a = u8(xq); a.as = u8(xs);
-    a.b0 = u8(w.gate); a.b0s = u8(w.gate_scales); a.b1 = u8(w.up); a.b1s = u8(w.up_scales);
+    a.as = u8(xs); a.b0s = u8(w.gate_scales); a.b1s = u8(w.up_scales);
     a.h = static_cast<uint8_t*>(hq); a.hs = static_cast<uint8_t*>(hs);
-    a.E = c.E; a.N = c.F; a.Kdim = c.D; a.max_rows = max_rows; a.nk = c.T * c.K; a.status = status;
-    ffn_mx8_simple_kernel<true><<<dim3((c.F + kSN - 1) / kSN, mt), 256, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    a.E = c.E; a.Kdim = c.D; a.N = c.F; a.n_tiles = (c.F + 127) / 128;
+    a.max_rows = max_rows; a.nk = c.T * c.K; a.status = status; a.amaps = gm;
+    cudaError_t e = pair ? launch_one<true, true>(mX, mG, mU, mY, a, mt * a.n_tiles, s)
+                         : launch_one<true, false>(mX, mG, mU, mY, a, mt * a.n_tiles, s);
     if (e != cudaSuccess) return e;
-    a.a = u8(hq); a.as = u8(hs);
-    a.b0 = u8(w.down); a.b0s = u8(w.down_scales);
+    a.as = u8(hs); a.b0s = a.b1s = u8(w.down_scales);
     a.y = static_cast<__nv_bfloat16*>(y_perm);
-    a.N = c.D; a.Kdim = c.F;
-    ffn_mx8_simple_kernel<false><<<dim3((c.D + kSN - 1) / kSN, mt), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    a.Kdim = c.F; a.N = c.D; a.n_tiles = (c.D + 255) / 256;
+    a.amaps = gm ? gm + c.E : nullptr;
+    return pair ? launch_one<false, true>(mH, mD, mD, mY, a, mt * a.n_tiles, s)
+                : launch_one<false, false>(mH, mD, mD, mY, a, mt * a.n_tiles, s);
 }
 
 }  // namespace moe

@@ -928,6 +928,17 @@ cudaError_t launch_ffn_tc_bf16(const moe_config& c, int64_t max_rows, const void
                 : launch_one<kDown, false>(mH, mD, mD, mYo, mYo, a2, mtiles_bound * a2.n_tiles, s);
 }
 
+// The per-expert A maps for the 8-bit experts (ffn_mx8.cu): two 2-D maps.
+cudaError_t launch_ffn_amaps(const void* map_x, const void* map_h, const int32_t* offsets, int E, int64_t max_rows,
+                             void* maps, cudaStream_t s)
+{
+    using namespace tc;
+    ffn_amaps_kernel<<<(E + 127) / 128, 128, 0, s>>>(*static_cast<const CUtensorMap*>(map_x),
+                                                     *static_cast<const CUtensorMap*>(map_h), offsets, E, max_rows, 0,
+                                                     static_cast<CUtensorMap*>(maps));
+    return cudaGetLastError();
+}
+
 cudaError_t launch_dgrad_tc_bf16(const moe_config& c, int64_t max_rows, const void* dyp,
                                  const int32_t* offsets, const void* gu, const void* w_gate,
                                  const void* w_up, const void* w_down, void* dgu, void* dxp,

@@ -385,10 +385,14 @@ def _experts_state(T, D, F, E, K, seed, counts=None, wscale=0.05):
         counts = torch.bincount(ids, minlength=E).tolist()
     offsets = torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int32, device="cuda")
     perm = torch.randperm(R, generator=g, device="cuda").to(torch.int32)
-    xq, xs = _quantize_ref(_randn(g, R, D))
+    def spread(*shape):  # every block at a scale of its own
+        v = _randn(g, *shape).unflatten(-1, (-1, 32))
+        k = torch.randint(-4, 5, (*v.shape[:-1], 1), generator=g, device="cuda")
+        return (v * torch.exp2(k.float())).flatten(-2)
+    xq, xs = _quantize_ref(spread(R, D))
     w = []
     for n, k in ((F, D), (F, D), (D, F)):
-        w += list(_quantize_ref(wscale * _randn(g, E, n, k)))
+        w += list(_quantize_ref(wscale / 16 * spread(E, n, k)))
     return dict(cfg=M.MoeConfig.make(T, D, F, E, K, "bf16"), xq=xq, xs=xs, offsets=offsets, perm=perm,
                 topk_w=torch.rand(T, K, generator=g, device="cuda"), w=tuple(w), counts=counts)
 
