@@ -483,6 +483,7 @@ MOE_API moe_status moe_mx8_workspace_size(const moe_config *cfg, size_t *bytes);
  *   y_perm[r, :] = topk_w[perm[r]] * (h[r] Wd_e)                  (bf16)
  * xq (max_rows, D) and xs (max_rows, D / 32): expert-major rows as mx8; hq
  * (max_rows, F) and hs (max_rows, F / 32): the intermediate, written here.
+ * hq and y_perm start on a 32-byte boundary (MOE_ERR_ALIGN otherwise).
  * perm and topk_w may both be NULL (weight 1).  Rows at and behind offsets[E]
  * are left as they were.  A NaN scale makes the rows that meet it NaN.
  */

@@ -8,6 +8,7 @@
 namespace moe {
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool al32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 static bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static moe_status check_scratch(const void* ws, size_t bytes, size_t need)
@@ -190,7 +191,8 @@ moe_status moe_expert_ffn_mx8(const moe_config* cfg, const void* xq, const void*
     if (st != MOE_OK) return st;
     if (!xq || !xs || !offsets || !hq || !hs || !y_perm) return MOE_ERR_ARG;
     if ((perm == nullptr) != (topk_w == nullptr)) return MOE_ERR_ARG;
-    if (!al16(xq) || !al16(xs) || !al16(hq) || !al16(hs) || !al16(y_perm)) return MOE_ERR_ALIGN;
+    if (!al16(xq) || !al16(xs) || !al16(hs)) return MOE_ERR_ALIGN;
+    if (!al32(hq) || !al32(y_perm)) return MOE_ERR_ALIGN;  // stored 32 bytes at a time
     st = check_scratch(workspace, workspace_bytes, mx8_ws_bytes(*cfg));
     if (st != MOE_OK) return st;
     return cuda_status(launch_ffn_mx8(*cfg, max_rows_of(*cfg), xq, xs, offsets, perm, topk_w, *weights, hq, hs,

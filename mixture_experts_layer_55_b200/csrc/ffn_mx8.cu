@@ -17,15 +17,26 @@
 //   warp 0       TMA producer: A 128 x 128 and B 256 (pair: 128) x 128 bytes
 //   warp 1       MMA issuer (pair: the leader's); owns the tensor memory
 //   warps 2..5   scales: a thread per row of A and two of B loads the scales of
-//                four stages at once (16 bytes of a row where rows allow it),
-//                one such group ahead, and writes each stage's as 32 x 16-byte
-//                blocks [row % 32][row / 32][4 of K]; tcgen05.cp replicates them
-//                over the four lane quadrants of tensor memory
+//                four stages at once (16 bytes of a row where rows allow it), two
+//                such groups ahead, and writes each stage's as 32 x 16-byte blocks
+//                [row % 32][row / 32][4 of K] into a ring of four groups;
+//                tcgen05.cp replicates them over the four lane quadrants of
+//                tensor memory
 //   warps 6..13  epilogue: two per lane quadrant, each half of the columns
 // Tensor memory: two accumulators of 256 columns and the scales do not fit 512
 // columns, so the accumulators overlap by 32 (0..255 and 224..479, scales from
 // 480).  The epilogue empties the shared columns first and says so; the next
 // tile's MMAs start then, not when the whole accumulator has been read.
+//
+// Bound: the tensor cores (few, long experts), the stream of weights (decode).
+// Measured on the way (T = 4096, D = F = 4096, 8 experts, K = 2; gate/up and
+// down in us): 461 + 232 with a release at cluster scope for every stage's
+// scales; 351 + 182 with one for every four stages, issued by an idle thread;
+// 276 + 141 with the issuing warp's operands in uniform registers; 232 + 126
+// with scales four groups deep and 32-byte stores.  The MMAs alone take
+// 184 + 97, the loads alone 165 + 84.  T = 8192, D = 4096, F = 14336: 1.49 + 0.76
+// ms, 2570 TFLOP/s.  256 experts, D = 7168, F = 2048, 128 tokens:
+// 1.16 + 0.60 ms, 6.6 TB/s.
 #include <cuda.h>
 
 #include "internal.h"
@@ -41,15 +52,18 @@ namespace mx {
 
 constexpr int BK = 128;                // contracted elements (bytes) per stage
 constexpr int A_BYTES = 128 * BK;
-constexpr int SF_BYTES = 3 * 512;      // scales of 128 rows of A and 256 of B, 4 per row
+constexpr int SF_BYTES = 3 * 512;      // a stage's scales: 128 rows of A and 256 of B, 4 per row
+constexpr int SF_GROUP = 4;            // stages whose scales arrive together (1, 2 or 4)
+constexpr int SF_SLOTS = 16 / SF_GROUP;  // groups in shared memory
+constexpr int SF_SLOT_BYTES = SF_GROUP * SF_BYTES;
 constexpr int ACC_STRIDE = 224;        // second accumulator's first column
-constexpr int SF_COL = 480;            // A's scales: 4 columns, then B's 8
+constexpr int SF_COL = 480;            // scales: two buffers, A's 4 columns, then B's 8
+constexpr int SF_BUF_COLS = 16;
 constexpr int TMEM_COLS = 512;
 constexpr int SF_WARPS = 4;
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 2 + SF_WARPS;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-constexpr int OUT_BYTES = 2048;        // an epilogue warp's 32 x 32 bf16 piece (down)
 constexpr int MAX_E = 256;
 
 template <bool PAIR> struct Geo {
@@ -63,8 +77,9 @@ template <bool PAIR> struct Geo {
 
 struct Misc {
     uint64_t full[8];
-    uint64_t sfull[8];    // the stage's scales are in shared memory (both CTAs')
     uint64_t empty[8];
+    uint64_t sfull[SF_SLOTS];   // a group's scales are in shared memory (both CTAs')
+    uint64_t sempty[SF_SLOTS];  // and have been copied to tensor memory
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t tover;       // the accumulators' shared columns have been read
@@ -78,7 +93,7 @@ struct Misc {
 
 template <bool PAIR> constexpr size_t smem_bytes()
 {
-    return 1024 + (size_t)Geo<PAIR>::STAGES * (Geo<PAIR>::OP_BYTES + SF_BYTES) + EPI_WARPS * OUT_BYTES + sizeof(Misc);
+    return 1024 + (size_t)Geo<PAIR>::STAGES * Geo<PAIR>::OP_BYTES + SF_SLOTS * SF_SLOT_BYTES + sizeof(Misc);
 }
 
 struct Args {
@@ -103,36 +118,85 @@ MOE_DEVICE constexpr uint32_t mx_idesc(int M, int N)
     return (1u << 23) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The issuing warp runs as a whole (its operands stay in uniform registers) and
+// one elected lane (`leader`) issues: with a single-lane branch around the loop
+// instead, moving the operands took 80 cycles for each MMA, more than half of
+// the MMA itself, and bound the kernel.
 template <bool PAIR>
-MOE_DEVICE void mma_mx8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                        uint32_t accumulate)
+MOE_DEVICE void mma_mx8(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                        uint32_t sfb, uint32_t accumulate)
 {
     if (PAIR)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(leader)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(leader)
             : "memory");
 }
 
 // 32 x 16 bytes of shared memory to four columns, replicated over the lane
 // quadrants (pair: in both CTAs, each from its own shared memory).
-template <bool PAIR> MOE_DEVICE void copy_scales(uint32_t taddr, uint64_t desc)
+template <bool PAIR> MOE_DEVICE void copy_scales(uint32_t leader, uint32_t taddr, uint64_t desc)
 {
-    if (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    if (PAIR)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                     "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(leader)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                     "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc), "r"(leader)
+                     : "memory");
+}
+
+// Arrive on the barrier (pair: at this offset in both CTAs) once every tensor
+// instruction that the elected lane has issued so far is done.
+template <bool PAIR> MOE_DEVICE void commit(uint32_t leader, uint32_t bar)
+{
+    if (PAIR)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                     "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+                     "h"((uint16_t)0x3), "r"(leader)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                     "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                     "r"(leader)
+                     : "memory");
 }
 
 // Descriptor of a block of scales: no swizzle, groups of 8 rows 128 bytes apart.
 MOE_DEVICE uint64_t scale_desc(uint32_t smem_addr)
 {
     return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1u << 46);
+}
+
+// All lanes wait, and agree on the outcome.
+MOE_DEVICE bool warp_wait_all(uint64_t* bar, uint32_t parity, int* status, int where, volatile int* abort_flag)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, where, abort_flag));
+}
+
+// One lane waits for the warp.
+MOE_DEVICE bool warp_wait(uint64_t* bar, uint32_t parity, int lane, int* status, int where, volatile int* abort_flag)
+{
+    int ok = 1;
+    if (lane == 0) ok = mbar_wait(bar, parity, status, where, abort_flag) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// Arrival on the leader's barrier that says tensor memory has been read (the
+// loads are complete: tcgen05.wait::ld).  No memory is published with it, so it
+// needs no release at cluster scope, which costs about 1000 cycles here.
+MOE_DEVICE void arrive_read(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // ----------------------------------------------------------------- tiles --
@@ -181,6 +245,14 @@ MOE_DEVICE uint32_t word_of(const uint4& v, int i)
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// 32 bytes at a 32-byte boundary in one store: a whole sector per lane.
+MOE_DEVICE void store32(void* p, const uint32_t* v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // silu(g) u in fp32: the exponential and the quotient to 2^-21, so that the one
 // rounding of h is the 8-bit one.
 MOE_DEVICE float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
@@ -188,16 +260,15 @@ MOE_DEVICE float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-
 template <bool GATEUP, bool PAIR>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     ffn_mx8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                   const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmY, const Args a)
+                   const __grid_constant__ CUtensorMap tmB1, const Args a)
 {
     using G = Geo<PAIR>;
     constexpr int BM = G::BM, BN = GATEUP ? 128 : 256, STAGES = G::STAGES, OP_BYTES = G::OP_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stages = smem;
-    uint8_t* outbuf = smem + (size_t)STAGES * OP_BYTES;
-    uint8_t* scales = outbuf + (size_t)EPI_WARPS * OUT_BYTES;
-    Misc* m = reinterpret_cast<Misc*>(scales + (size_t)STAGES * SF_BYTES);
+    uint8_t* scales = smem + (size_t)STAGES * OP_BYTES;
+    Misc* m = reinterpret_cast<Misc*>(scales + (size_t)SF_SLOTS * SF_SLOT_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = a.E;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;  // 0: the leader, which issues the MMAs
@@ -207,8 +278,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&m->full[s], 1);
-            mbar_init(&m->sfull[s], SF_WARPS * G::CTAS);
             mbar_init(&m->empty[s], 1);
+        }
+        for (int s = 0; s < SF_SLOTS; ++s) {
+            mbar_init(&m->sfull[s], SF_WARPS + (PAIR && rank == 0 ? 1 : 0));  // leader: and the peer's
+            mbar_init(&m->sempty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&m->tfull[b], 1);
@@ -221,7 +295,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB0);
         if (GATEUP) prefetch_tmap(&tmB1);
-        else prefetch_tmap(&tmY);
     }
     if (warp == 1) {
         if (PAIR) {
@@ -332,62 +405,97 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (last_phase[s] >= 0) mbar_wait(&m->full[s], (uint32_t)last_phase[s], a.status, 723, nullptr);
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // ------------------------------------------------ MMA issuer (leader only)
+        if (rank == 0) {
+            // ------------------------------------------------ MMA issuer (leader CTA only)
             constexpr uint32_t idesc = mx_idesc(BM, 256);
-            int stage = 0;
-            uint32_t phase = 0;
-            int acc = 0;
-            uint32_t acc_phase = 0, over_phase = 1;  // no tile before the first one
+            const uint32_t leader = elect_one();
+            const uint32_t tbase = __shfl_sync(0xffffffffu, tmem_base, 0);
+            const int tiles = __shfl_sync(0xffffffffu, total, 0);
+            const uint32_t s_stages = __shfl_sync(0xffffffffu, smem_u32(stages), 0);
+            const uint32_t s_scales = __shfl_sync(0xffffffffu, smem_u32(scales), 0);
+            const uint32_t s_empty = __shfl_sync(0xffffffffu, smem_u32(&m->empty[0]), 0);
+            const uint32_t s_sempty = __shfl_sync(0xffffffffu, smem_u32(&m->sempty[0]), 0);
+            const uint32_t s_tfull = __shfl_sync(0xffffffffu, smem_u32(&m->tfull[0]), 0);
+            int stage = 0, acc = 0, slot = 0, in_slot = 0;
+            uint32_t phase = 0, acc_phase = 0, sphase = 0, over_phase = 1;  // no tile before the first one
             bool ok = true;
-            for (int t = unit; t < total && ok; t += units) {
+            for (int t = unit; t < tiles && ok; t += units) {
                 // this accumulator's last tile has been read, and the shared
                 // columns of the tile before this one
-                if (!mbar_wait(&m->tempty[acc], acc_phase ^ 1u, a.status, 724, abort_flag)) break;
-                if (!mbar_wait(&m->tover, over_phase, a.status, 725, abort_flag)) break;
+                if (!warp_wait_all(&m->tempty[acc], acc_phase ^ 1u, a.status, 724, abort_flag)) break;
+                if (!warp_wait_all(&m->tover, over_phase, a.status, 725, abort_flag)) break;
                 over_phase ^= 1u;
                 tc_fence_after();
-                const uint32_t d0 = tmem_base + (uint32_t)(acc * ACC_STRIDE);
+                const uint32_t d0 = tbase + (uint32_t)(acc * ACC_STRIDE);
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(&m->full[stage], phase, a.status, 726, abort_flag) ||
-                        !mbar_wait(&m->sfull[stage], phase, a.status, 727, abort_flag)) {
+                    if (in_slot == 0 && !warp_wait_all(&m->sfull[slot], sphase, a.status, 727, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!warp_wait_all(&m->full[stage], phase, a.status, 726, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sA = smem_u32(stages + (size_t)stage * OP_BYTES);
-                    const uint32_t sB = sA + A_BYTES;
-                    const uint32_t sS = smem_u32(scales + (size_t)stage * SF_BYTES);
                     // the copies and the MMAs of one thread run in order
-                    const uint32_t tsa = tmem_base + SF_COL, tsb = tsa + 4;
-                    copy_scales<PAIR>(tsa, scale_desc(sS));
-                    copy_scales<PAIR>(tsb, scale_desc(sS + 512));
-                    copy_scales<PAIR>(tsb + 4, scale_desc(sS + 1024));
+                    const uint32_t tsa = tbase + SF_COL + (uint32_t)((kb & 1) * SF_BUF_COLS);
+                    const uint64_t sdesc = scale_desc(s_scales + (uint32_t)(slot * SF_SLOT_BYTES + in_slot * SF_BYTES));
+                    copy_scales<PAIR>(leader, tsa, sdesc);
+                    copy_scales<PAIR>(leader, tsa + 4, sdesc + (512 >> 4));
+                    copy_scales<PAIR>(leader, tsa + 8, sdesc + (1024 >> 4));
+                    const uint64_t adesc = umma_desc_sw128(s_stages + (uint32_t)stage * OP_BYTES, 16, 1024);
+                    const uint64_t bdesc = adesc + (A_BYTES >> 4);
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk)
-                        mma_mx8<PAIR>(d0, umma_desc_sw128(sA + kk * 32, 16, 1024), umma_desc_sw128(sB + kk * 32, 16, 1024),
-                                      idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), tsa, tsb,
-                                      (kb | kk) != 0 ? 1u : 0u);
+                        mma_mx8<PAIR>(leader, d0, adesc + kk * 2, bdesc + kk * 2,
+                                      idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), tsa, tsa + 4,
+                                      kk != 0 ? 1u : (kb != 0 ? 1u : 0u));
                     // frees the stage (in both CTAs) once these complete
-                    if (PAIR) umma_commit_pair_mc(&m->empty[stage], 0x3);
-                    else umma_commit(&m->empty[stage]);
+                    commit<PAIR>(leader, s_empty + (uint32_t)stage * 8);
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    if (++in_slot == SF_GROUP || kb == num_kb - 1) {  // and the group's scales
+                        commit<PAIR>(leader, s_sempty + (uint32_t)slot * 8);
+                        in_slot = 0;
+                        if (++slot == SF_SLOTS) {
+                            slot = 0;
+                            sphase ^= 1u;
+                        }
+                    }
                 }
                 if (!ok) break;
-                if (PAIR) umma_commit_pair_mc(&m->tfull[acc], 0x3);
-                else umma_commit(&m->tfull[acc]);
+                commit<PAIR>(leader, s_tfull + (uint32_t)acc * 8);
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
             // every MMA issued here is done before the allocation is released
-            if (PAIR) umma_commit_pair_mc(&m->drain, 0x1);
-            else umma_commit(&m->drain);
-            mbar_wait(&m->drain, 0, a.status, 728, nullptr);
+            __syncwarp();
+            if (leader) {
+                if (PAIR) umma_commit_pair_mc(&m->drain, 0x1);
+                else umma_commit(&m->drain);
+            }
+            __syncwarp();
+            warp_wait_all(&m->drain, 0, a.status, 728, nullptr);
+        } else if (PAIR && lane == 0) {
+            // ------------------------------------------------ the peer: its scales' arrival, passed on
+            // The release at cluster scope that makes them the leader's to use
+            // waits for the issuing thread's own memory traffic, about 1000 cycles
+            // in a thread that loads scales; this one has none.
+            int slot = 0;
+            uint32_t sphase = 0;
+            const int64_t mine = unit < total ? (int64_t)((total - unit + units - 1) / units) * ((num_kb + SF_GROUP - 1) / SF_GROUP) : 0;
+            for (int64_t n = 0; n < mine; ++n) {
+                if (!mbar_wait(&m->sfull[slot], sphase, a.status, 731, abort_flag)) break;
+                mbar_arrive_cluster(mapa_shared(smem_u32(&m->sfull[slot]), 0));
+                if (++slot == SF_SLOTS) {
+                    slot = 0;
+                    sphase ^= 1u;
+                }
+            }
         }
     } else if (warp < EPI_WARP0) {
         // ------------------------------------------------ scales (each CTA: its A rows, all of B's)
@@ -408,59 +516,59 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             pb0 = n < a.N ? bs + (be + n) * nb : nullptr;
             pb1 = n2 < a.N ? bs + (be + n2) * nb : nullptr;
         };
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        uint4 va = make_uint4(0, 0, 0, 0), v0 = va, v1 = va;
-        if (unit < total) {
-            rows_of(unit);
-            va = load_scales(pa, 0, nb);
-            v0 = load_scales(pb0, 0, nb);
-            v1 = load_scales(pb1, 0, nb);
-        }
-        for (int t = unit; t < total && ok; t += units) {
-            for (int g = 0; g < groups && ok; ++g) {
-                // the next group's loads, of this tile or of the next one
-                uint4 na = make_uint4(0, 0, 0, 0), n0v = na, n1v = na;
-                int ng = g + 1;
-                bool more = true;
-                if (ng == groups) {
-                    ng = 0;
-                    more = t + units < total;
-                    if (more) rows_of(t + units);
-                }
-                if (more) {
-                    na = load_scales(pa, ng, nb);
-                    n0v = load_scales(pb0, ng, nb);
-                    n1v = load_scales(pb1, ng, nb);
-                }
-                const int kbs = num_kb - 4 * g < 4 ? num_kb - 4 * g : 4;
+        // two groups of loads in flight; a group's are long done when the fence of
+        // the one before it, which waits for loads too, is reached
+        uint4 va[2], v0[2], v1[2];
+        int ld_t = unit, ld_g = 0;
+        auto load_next = [&](int i2) {
+            if (ld_t >= total) return;
+            if (ld_g == 0) rows_of(ld_t);
+            va[i2] = load_scales(pa, ld_g, nb);
+            v0[i2] = load_scales(pb0, ld_g, nb);
+            v1[i2] = load_scales(pb1, ld_g, nb);
+            if (++ld_g == groups) {
+                ld_g = 0;
+                ld_t += units;
+            }
+        };
+        load_next(0);
+        load_next(1);
+        int slot = 0, kb_left = num_kb;
+        uint32_t sphase = 0;
+        const int64_t mine = unit < total ? (int64_t)((total - unit + units - 1) / units) * groups : 0;
+        for (int64_t n = 0; n < mine; n += 2) {
+            bool ok = true;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k >= kbs) break;
-                    if (!__all_sync(0xffffffffu, mbar_wait(&m->empty[stage], phase ^ 1u, a.status, 729, abort_flag))) {
+            for (int i2 = 0; i2 < 2; ++i2) {
+                if (n + i2 >= mine) break;
+#pragma unroll
+                for (int h = 0; h < 4 / SF_GROUP; ++h) {
+                    if (kb_left <= h * SF_GROUP) break;  // the tile's last stages
+                    if (!warp_wait(&m->sempty[slot], sphase ^ 1u, lane, a.status, 729, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* dst = scales + (size_t)stage * SF_BYTES + off;
-                    *reinterpret_cast<uint32_t*>(dst) = word_of(va, k);
-                    *reinterpret_cast<uint32_t*>(dst + 512) = word_of(v0, k);
-                    *reinterpret_cast<uint32_t*>(dst + 1024) = word_of(v1, k);
+                    uint8_t* dst = scales + (size_t)slot * SF_SLOT_BYTES + off;
+#pragma unroll
+                    for (int k = 0; k < SF_GROUP; ++k) {
+                        *reinterpret_cast<uint32_t*>(dst + k * SF_BYTES) = word_of(va[i2], h * SF_GROUP + k);
+                        *reinterpret_cast<uint32_t*>(dst + k * SF_BYTES + 512) = word_of(v0[i2], h * SF_GROUP + k);
+                        *reinterpret_cast<uint32_t*>(dst + k * SF_BYTES + 1024) = word_of(v1[i2], h * SF_GROUP + k);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&m->sfull[stage]), 0));
-                        else mbar_arrive(&m->sfull[stage]);
-                    }
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                    if (lane == 0) mbar_arrive(&m->sfull[slot]);
+                    if (++slot == SF_SLOTS) {
+                        slot = 0;
+                        sphase ^= 1u;
                     }
                 }
-                va = na;
-                v0 = n0v;
-                v1 = n1v;
+                if (!ok) break;
+                kb_left -= 4;
+                if (kb_left <= 0) kb_left = num_kb;
+                load_next(i2);
             }
+            if (!ok) break;
         }
     } else {
         // ------------------------------------------------ epilogue (each CTA, its 128 rows)
@@ -470,18 +578,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t tempty0 = mapa_shared(smem_u32(&m->tempty[0]), 0);
         const uint32_t tempty1 = mapa_shared(smem_u32(&m->tempty[1]), 0);
         const uint32_t tover = mapa_shared(smem_u32(&m->tover), 0);
-        uint8_t* obuf = outbuf + (size_t)(warp - EPI_WARP0) * OUT_BYTES;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int t = unit; t < total; t += units) {
             int e, m_row0, row_end, n0;
             decode_tile(m, E, BM, BN, t, e, m_row0, row_end, n0);
-            if (!__all_sync(0xffffffffu, mbar_wait(&m->tfull[acc], acc_phase, a.status, 730, abort_flag))) break;
+            if (!warp_wait(&m->tfull[acc], acc_phase, lane, a.status, 730, abort_flag)) break;
             tc_fence_after();
             const int64_t row = (int64_t)m_row0 + r_in_tile;
             const bool valid = row < row_end;
-            const int64_t warp_row0 = (int64_t)m_row0 + (int)rank * 128 + quad * 32;
-            const bool warp_full = warp_row0 + 32 <= row_end;
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * ACC_STRIDE);
             // the shared columns: the last 32 of accumulator 0, the first 32 of 1
             const bool shared_half = half == (acc == 0 ? 1 : 0);
@@ -510,7 +615,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(tover);
+                        if (PAIR) arrive_read(tover);
                         else mbar_arrive(&m->tover);
                     }
                 }
@@ -530,9 +635,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         for (int j = 0; j < 8; ++j)
                             p[j] = mx_pack4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), inv);
-                        uint4* dst = reinterpret_cast<uint4*>(a.h + row * a.N + col);
-                        dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
-                        dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                        store32(a.h + row * a.N + col, p);
                         a.hs[row * (a.N / kMxBlock) + col / kMxBlock] = (uint8_t)b;
                     }
                 } else if (col < a.N) {
@@ -540,32 +643,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         p[j] = pack_bf16x2(w * __uint_as_float(v[2 * j]), w * __uint_as_float(v[2 * j + 1]));
-                    if (warp_full) {  // through shared memory (64-byte swizzle) and a TMA store
-                        if (lane == 0) bulk_wait_read<0>();
-                        __syncwarp();
-                        uint4* dst = reinterpret_cast<uint4*>(obuf + lane * 64);
-                        const int sw = (lane >> 1) & 3;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            dst[q ^ sw] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(&tmY, obuf, col, (int)warp_row0);
-                            bulk_commit();
-                        }
-                    } else if (valid) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.y + row * a.N + col);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            dst[q] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+                    if (valid) {
+                        store32(a.y + row * a.N + col, p);
+                        store32(a.y + row * a.N + col + 16, p + 8);
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(acc == 0 ? tempty0 : tempty1);
+                if (PAIR) arrive_read(acc == 0 ? tempty0 : tempty1);
                 else mbar_arrive(&m->tempty[acc]);
             }
             if (++acc == 2) {
@@ -573,8 +660,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 acc_phase ^= 1u;
             }
         }
-        if (lane == 0) bulk_wait_all<0>();  // every store of this warp has completed
-        __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
@@ -623,20 +708,6 @@ static bool map_bytes(CUtensorMap* m, const void* base, uint64_t K, uint64_t row
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// y (rows, cols) bf16 for 32 x 32 stores from shared memory (64-byte swizzle)
-static bool map_store(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows)
-{
-    EncodeTiledFn enc = encoder();
-    if (!enc) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * 2};
-    cuuint32_t box[2] = {32, 32};
-    cuuint32_t es[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Per device: shared memory opted in, and how many CTAs or pairs are resident.
 template <bool GATEUP, bool PAIR> static cudaError_t prepare(int* resident)
 {
@@ -680,7 +751,7 @@ template <bool GATEUP, bool PAIR> static cudaError_t prepare(int* resident)
 
 template <bool GATEUP, bool PAIR>
 static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, const CUtensorMap& mB1,
-                              const CUtensorMap& mY, const Args& a, int64_t tiles_bound, cudaStream_t s)
+                              const Args& a, int64_t tiles_bound, cudaStream_t s)
 {
     int units = 0;
     cudaError_t e = prepare<GATEUP, PAIR>(&units);
@@ -689,7 +760,7 @@ static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, con
     if (n < 1) n = 1;
     constexpr size_t smem = smem_bytes<PAIR>();
     if (!PAIR) {
-        ffn_mx8_kernel<GATEUP, false><<<(unsigned)n, NUM_THREADS, smem, s>>>(mA, mB0, mB1, mY, a);
+        ffn_mx8_kernel<GATEUP, false><<<(unsigned)n, NUM_THREADS, smem, s>>>(mA, mB0, mB1, a);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
@@ -704,7 +775,7 @@ static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, con
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, true>, mA, mB0, mB1, mY, a);
+    return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, true>, mA, mB0, mB1, a);
 }
 
 }  // namespace mx
@@ -717,10 +788,10 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
     using namespace mx;
     auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
     const uint64_t D = (uint64_t)c.D, F = (uint64_t)c.F, E = (uint64_t)c.E, R = (uint64_t)max_rows;
-    CUtensorMap mX, mG, mU, mH, mD, mY;
+    CUtensorMap mX, mG, mU, mH, mD;
     if (!map_bytes(&mX, xq, D, R, 0, 128) || !map_bytes(&mG, w.gate, D, F, E, 64) ||
         !map_bytes(&mU, w.up, D, F, E, 64) || !map_bytes(&mH, hq, F, R, 0, 128) ||
-        !map_bytes(&mD, w.down, F, D, E, 64) || !map_store(&mY, y_perm, D, R))
+        !map_bytes(&mD, w.down, F, D, E, 64))
         return cudaErrorInvalidValue;
     // CTA pairs when experts hold 128 rows or more on average, as the bf16
     // experts: single CTAs waste fewer padded rows on a few tokens each
@@ -741,15 +812,15 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
     a.h = static_cast<uint8_t*>(hq); a.hs = static_cast<uint8_t*>(hs);
     a.E = c.E; a.Kdim = c.D; a.N = c.F; a.n_tiles = (c.F + 127) / 128;
     a.max_rows = max_rows; a.nk = c.T * c.K; a.status = status; a.amaps = gm;
-    cudaError_t e = pair ? launch_one<true, true>(mX, mG, mU, mY, a, mt * a.n_tiles, s)
-                         : launch_one<true, false>(mX, mG, mU, mY, a, mt * a.n_tiles, s);
+    cudaError_t e = pair ? launch_one<true, true>(mX, mG, mU, a, mt * a.n_tiles, s)
+                         : launch_one<true, false>(mX, mG, mU, a, mt * a.n_tiles, s);
     if (e != cudaSuccess) return e;
     a.as = u8(hs); a.b0s = a.b1s = u8(w.down_scales);
     a.y = static_cast<__nv_bfloat16*>(y_perm);
     a.Kdim = c.F; a.N = c.D; a.n_tiles = (c.D + 255) / 256;
     a.amaps = gm ? gm + c.E : nullptr;
-    return pair ? launch_one<false, true>(mH, mD, mD, mY, a, mt * a.n_tiles, s)
-                : launch_one<false, false>(mH, mD, mD, mY, a, mt * a.n_tiles, s);
+    return pair ? launch_one<false, true>(mH, mD, mD, a, mt * a.n_tiles, s)
+                : launch_one<false, false>(mH, mD, mD, a, mt * a.n_tiles, s);
 }
 
 }  // namespace moe

@@ -109,6 +109,8 @@ def test_expert_ffn_mx8_refusals(lib):
     assert call(cfg=_cfg(F=72)) == B.MOE_ERR_ALIGN
     assert call(cfg=_cfg(K=9, E=16)) == B.MOE_ERR_ARG
     assert call(xs=FAKE + 4) == B.MOE_ERR_ALIGN
+    assert call(hq=FAKE + 16) == B.MOE_ERR_ALIGN  # these two on 32 bytes
+    assert call(y=FAKE + 16) == B.MOE_ERR_ALIGN
     assert call(ws=None) == B.MOE_ERR_WORKSPACE
     assert call(nb=B.mx8_workspace_size(c) - 1) == B.MOE_ERR_WORKSPACE
     assert call(ws=FAKE + 64) == B.MOE_ERR_ALIGN
