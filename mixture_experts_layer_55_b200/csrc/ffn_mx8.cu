@@ -583,20 +583,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int t = unit; t < total; t += units) {
             int e, m_row0, row_end, n0;
             decode_tile(m, E, BM, BN, t, e, m_row0, row_end, n0);
-            if (!warp_wait(&m->tfull[acc], acc_phase, lane, a.status, 730, abort_flag)) break;
-            tc_fence_after();
             const int64_t row = (int64_t)m_row0 + r_in_tile;
             const bool valid = row < row_end;
-            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * ACC_STRIDE);
-            // the shared columns: the last 32 of accumulator 0, the first 32 of 1
-            const bool shared_half = half == (acc == 0 ? 1 : 0);
-            float w = 1.f;
+            float w = 1.f;  // the row's weight, loaded while the tile is computed
             if (!GATEUP && valid && a.perm != nullptr) {
                 const int32_t pa = a.perm[row];
                 w = 0.f;
                 if (pa >= 0 && (int64_t)pa < a.nk) w = a.topk_w[pa];
                 else if (half == 0) raise_flag(a.status, kFlagBounds, 721);
             }
+            if (!warp_wait(&m->tfull[acc], acc_phase, lane, a.status, 730, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * ACC_STRIDE);
+            // the shared columns: the last 32 of accumulator 0, the first 32 of 1
+            const bool shared_half = half == (acc == 0 ? 1 : 0);
             constexpr int CHUNKS = GATEUP ? 2 : 4;
 #pragma unroll 1
             for (int cc = 0; cc < CHUNKS; ++cc) {
