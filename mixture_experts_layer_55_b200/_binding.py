@@ -446,14 +446,15 @@ def _nbytes(t) -> int:
 # stream, or to the current stream of the tensors' device.
 
 def _check_tensors(where, specs):
-    """specs: (name, tensor or None, dtype names, elements).  Returns the device
-    index they share."""
-    import torch
+    """specs: (name, tensor or None, dtypes, elements).  Returns the device index the
+    tensors share and their addresses (None for None)."""
     dev = None
+    ptrs = []
     for name, t, dtypes, numel in specs:
         if t is None:
+            ptrs.append(None)
             continue
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _TENSOR):
             raise ValueError(f"{where}: {name} must be a tensor")
         if t.dtype not in dtypes:
             raise ValueError(f"{where}: {name} has dtype {t.dtype}")
@@ -462,42 +463,44 @@ def _check_tensors(where, specs):
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
         d = t.get_device()
-        if dev is None:
+        if d != dev:
+            if dev is not None:
+                raise ValueError(f"{where}: {name} is on another device than the other tensors")
             dev = d
-        elif d != dev:
-            raise ValueError(f"{where}: {name} is on another device than the other tensors")
+        ptrs.append(t.data_ptr())
     if dev is None or dev < 0:
         raise ValueError(f"{where}: the tensors must be on a CUDA device")
-    return dev
+    return dev, ptrs
 
 
 def _run(where, dev, fn, args, stream):
     """fn(*args, stream) on device dev."""
     import torch
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, _stream(stream))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
+            st = fn(*args, stream)
     if st != MOE_OK:
         raise MoEError(st, where)
 
 
-def _layer_types():
-    import torch
-    return {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
-
-
 _TYPES = None
+_TENSOR = ()
 
 
 def _types():
     """(layer dtypes -> moe_dtype, fp32, int32, the dtypes of 8-bit values, of bytes)"""
-    global _TYPES
+    global _TYPES, _TENSOR
     if _TYPES is None:
         import torch
-        _TYPES = (_layer_types(), (torch.float32,), (torch.int32,), (torch.float8_e4m3fn, torch.uint8),
-                  (torch.uint8, torch.bool, torch.float8_e8m0fnu))
+        _TENSOR = torch.Tensor
+        _TYPES = ({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}, (torch.float32,), (torch.int32,),
+                  (torch.float8_e4m3fn, torch.uint8), (torch.uint8, torch.bool, torch.float8_e8m0fnu))
     return _TYPES
 
 
@@ -516,12 +519,11 @@ def moe_rmsnorm(x, gamma, n, residual=None, s=None, rstd=None, q=None, q_scales=
     layer, f32, _, q8, byte = _types()
     T, D, dt = _rows("moe_rmsnorm", "x", x, layer)
     nel = T * D
-    dev = _check_tensors("moe_rmsnorm", (
+    dev, p = _check_tensors("moe_rmsnorm", (
         ("x", x, dt, nel), ("gamma", gamma, f32, D), ("n", n, dt, nel), ("residual", residual, dt, nel),
         ("s", s, dt, nel), ("rstd", rstd, f32, T), ("q", q, q8, nel), ("q_scales", q_scales, byte, nel // 32)))
     _run("moe_rmsnorm", dev, lib().moe_rmsnorm,
-         (T, D, layer[x.dtype], _ptr(x), _ptr(residual), _ptr(gamma), eps, _ptr(s), _ptr(n), _ptr(rstd), _ptr(q),
-          _ptr(q_scales)), stream)
+         (T, D, layer[x.dtype], p[0], p[3], p[1], eps, p[4], p[2], p[5], p[6], p[7]), stream)
 
 
 def rmsnorm_backward_workspace_size(T: int, D: int) -> int:
@@ -537,33 +539,32 @@ def moe_rmsnorm_backward(dn, s, gamma, rstd, dx, dgamma, workspace, ds=None, str
     layer, f32, _, _, byte = _types()
     T, D, dt = _rows("moe_rmsnorm_backward", "s", s, layer)
     nel = T * D
-    dev = _check_tensors("moe_rmsnorm_backward", (
+    dev, p = _check_tensors("moe_rmsnorm_backward", (
         ("s", s, dt, nel), ("dn", dn, dt, nel), ("gamma", gamma, f32, D), ("rstd", rstd, f32, T),
         ("dx", dx, dt, nel), ("dgamma", dgamma, f32, D), ("ds", ds, dt, nel),
         ("workspace", workspace, byte, workspace.numel())))
     _run("moe_rmsnorm_backward", dev, lib().moe_rmsnorm_backward,
-         (T, D, layer[s.dtype], _ptr(dn), _ptr(ds), _ptr(s), _ptr(gamma), _ptr(rstd), _ptr(dx), _ptr(dgamma),
-          _ptr(workspace), workspace.numel()), stream)
+         (T, D, layer[s.dtype], p[1], p[6], p[0], p[2], p[3], p[4], p[5], p[7], workspace.numel()), stream)
 
 
 def moe_mx8_quantize(x, q, scales, stream=None):
     """x (rows, cols) bf16 or fp32 into q (rows, cols) e4m3 and scales (rows, cols / 32)."""
     layer, _, _, q8, byte = _types()
     T, D, dt = _rows("moe_mx8_quantize", "x", x, layer)
-    dev = _check_tensors("moe_mx8_quantize", (
+    dev, p = _check_tensors("moe_mx8_quantize", (
         ("x", x, dt, T * D), ("q", q, q8, T * D), ("scales", scales, byte, T * D // 32)))
     _run("moe_mx8_quantize", dev, lib().moe_mx8_quantize,
-         (T, D, layer[x.dtype], _ptr(x), _ptr(q), _ptr(scales)), stream)
+         (T, D, layer[x.dtype], *p), stream)
 
 
 def moe_mx8_dequantize(q, scales, out, stream=None):
     """The values of q (rows, cols) and scales (rows, cols / 32) into out, bf16 or fp32."""
     layer, _, _, q8, byte = _types()
     T, D, dt = _rows("moe_mx8_dequantize", "out", out, layer)
-    dev = _check_tensors("moe_mx8_dequantize", (
+    dev, p = _check_tensors("moe_mx8_dequantize", (
         ("out", out, dt, T * D), ("q", q, q8, T * D), ("scales", scales, byte, T * D // 32)))
     _run("moe_mx8_dequantize", dev, lib().moe_mx8_dequantize,
-         (T, D, layer[out.dtype], _ptr(q), _ptr(scales), _ptr(out)), stream)
+         (T, D, layer[out.dtype], p[1], p[2], p[0]), stream)
 
 
 def moe_mx8_prepare_weight(w, q, scales, stream=None):
@@ -573,10 +574,10 @@ def moe_mx8_prepare_weight(w, q, scales, stream=None):
     if getattr(w, "dim", None) is None or w.dim() != 3 or w.dtype not in layer:
         raise ValueError("moe_mx8_prepare_weight: w must be an (E, K, N) bf16 or fp32 tensor")
     E, K, N = w.shape
-    dev = _check_tensors("moe_mx8_prepare_weight", (
+    dev, p = _check_tensors("moe_mx8_prepare_weight", (
         ("w", w, (w.dtype,), E * K * N), ("q", q, q8, E * K * N), ("scales", scales, byte, E * K * N // 32)))
     _run("moe_mx8_prepare_weight", dev, lib().moe_mx8_prepare_weight,
-         (E, K, N, layer[w.dtype], _ptr(w), _ptr(q), _ptr(scales)), stream)
+         (E, K, N, layer[w.dtype], *p), stream)
 
 
 class Mx8Weights(ctypes.Structure):
@@ -605,16 +606,15 @@ def moe_expert_ffn_mx8(cfg, xq, xs, offsets, perm, topk_w, weights, hq, hs, y_pe
     writes them; hq, hs: the intermediate; y_perm (max_rows, D) bf16."""
     import torch
     _, f32, i32, q8, byte = _types()
-    R = max_rows(cfg)
-    dev = _check_tensors("moe_expert_ffn_mx8", [
+    R = max_rows(cfg) if cfg.capacity_factor > 0 else cfg.T * cfg.K
+    dev, p = _check_tensors("moe_expert_ffn_mx8", [
         ("xq", xq, q8, R * cfg.D), ("xs", xs, byte, R * cfg.D // 32), ("offsets", offsets, i32, cfg.E + 1),
         ("perm", perm, i32, R), ("topk_w", topk_w, f32, cfg.T * cfg.K), ("hq", hq, q8, R * cfg.F),
         ("hs", hs, byte, R * cfg.F // 32), ("y_perm", y_perm, (torch.bfloat16,), R * cfg.D),
         ("workspace", workspace, byte, workspace.numel())] + _mx8_specs(cfg, weights))
-    w = Mx8Weights(*(_ptr(t) for t in weights))
+    w = Mx8Weights(*p[9:])
     _run("moe_expert_ffn_mx8", dev, lib().moe_expert_ffn_mx8,
-         (_cfg(cfg), _ptr(xq), _ptr(xs), _ptr(offsets), _ptr(perm), _ptr(topk_w), ctypes.byref(w), _ptr(hq),
-          _ptr(hs), _ptr(y_perm), _ptr(workspace), workspace.numel()), stream)
+         (_cfg(cfg), *p[:5], ctypes.byref(w), *p[5:9], workspace.numel()), stream)
 
 
 def forward_mx8_workspace_size(cfg: MoeConfig) -> int:
@@ -632,7 +632,7 @@ def moe_forward_mx8(cfg, x, w_router, weights, y, workspace, xq=None, xs=None, y
     _, f32, i32, q8, byte = _types()
     T, D, E, K = cfg.T, cfg.D, cfg.E, cfg.K
     bf16 = (torch.bfloat16,)
-    dev = _check_tensors("moe_forward_mx8", [
+    dev, p = _check_tensors("moe_forward_mx8", [
         ("x", x, bf16, T * D), ("w_router", w_router, f32, D * E), ("y", y, bf16, T * D), ("xq", xq, q8, T * D),
         ("xs", xs, byte, T * D // 32), ("y_add", y_add, bf16, T * D), ("router_bias", router_bias, f32, E),
         ("selection_bias", selection_bias, f32, E), ("logit_noise", logit_noise, f32, T * E),
@@ -640,11 +640,10 @@ def moe_forward_mx8(cfg, x, w_router, weights, y, workspace, xq=None, xs=None, y
         ("mean_prob", mean_prob, f32, E), ("counts", counts, i32, E), ("topk_ids", topk_ids, i32, T * K),
         ("topk_w", topk_w, f32, T * K), ("workspace", workspace, byte, workspace.numel())]
         + _mx8_specs(cfg, weights))
-    w = Mx8Weights(*(_ptr(t) for t in weights))
+    w = Mx8Weights(*p[16:])
     _run("moe_forward_mx8", dev, lib().moe_forward_mx8,
-         (_cfg(cfg), _ptr(x), _ptr(xq), _ptr(xs), _ptr(w_router), _ptr(w_router_terms), _ptr(router_bias),
-          _ptr(selection_bias), _ptr(logit_noise), ctypes.byref(w), _ptr(y_add), _ptr(y), _ptr(losses),
-          _ptr(mean_prob), _ptr(counts), _ptr(topk_ids), _ptr(topk_w), _ptr(workspace), workspace.numel()), stream)
+         (_cfg(cfg), p[0], p[3], p[4], p[1], p[9], *p[6:9], ctypes.byref(w), p[5], p[2], *p[10:16],
+          workspace.numel()), stream)
 
 
 def balance_workspace_size(cfg: MoeConfig, S: int) -> int:
@@ -662,14 +661,14 @@ def moe_balance_loss(cfg, logits, topk_ids, seq_starts, counts, losses, seq_loss
     _, f32, i32, _, byte = _types()
     T, E = cfg.T, cfg.E
     S = seq_starts.numel() - 1
-    dev = _check_tensors("moe_balance_loss", (
+    dev, p = _check_tensors("moe_balance_loss", (
         ("logits", logits, f32, T * E), ("topk_ids", topk_ids, i32, T * cfg.K),
         ("seq_starts", seq_starts, i32, S + 1), ("counts", counts, i32, S * E), ("losses", losses, f32, 2),
         ("seq_loss", seq_loss, f32, S), ("token_mask", token_mask, byte, T), ("dlogits", dlogits, f32, T * E),
         ("workspace", workspace, byte, workspace.numel())))
     _run("moe_balance_loss", dev, lib().moe_balance_loss,
-         (_cfg(cfg), S, _ptr(logits), _ptr(topk_ids), _ptr(seq_starts), _ptr(token_mask), c_balance, c_z,
-          _ptr(counts), _ptr(losses), _ptr(seq_loss), _ptr(dlogits), _ptr(workspace), workspace.numel()), stream)
+         (_cfg(cfg), S, p[0], p[1], p[2], p[6], c_balance, c_z, p[3], p[4], p[5], p[7], p[8],
+          workspace.numel()), stream)
 
 
 def train_state_router(cfg: MoeConfig):

@@ -16,32 +16,34 @@
 // Sums do not depend on the order of the blocks: counts are integers; a
 // sequence's c_t, each in [0, 1], are added as integers of 2^-32 (half a step,
 // 2^-33, is far below fp32's own rounding of a c_t near 1/E >= 2^-8); z is summed
-// per block in fp64 and the blocks' sums are added in order by the last block.
+// per thread and block in fp64 and the blocks' sums are added in order by the
+// block that finishes last.
+//
+// One cooperative launch (every block resident): zero the results, count, and the
+// gradient, with two grid barriers between them.  Both are split: a block
+// arrives, does what does not depend on the others (its histogram in shared
+// memory; its first tokens' softmax), and then waits.  A block takes consecutive
+// tokens, a token a group of L lanes with 8 experts each, so that a warp is full
+// for 8 experts as for 256.  Bound: latency (launch, two barriers, a handful of
+// dependent loads) up to a few megabytes of logits, then HBM.
+//
 #include "internal.h"
 #include "common.cuh"
 
 namespace moe {
 
-constexpr int kBalTokens = 32;     // tokens per block of the gradient pass (8 warps)
-constexpr int kBalPerLane = 8;     // experts per lane: E <= 256
+constexpr int kBalThreads = 256;
+constexpr int kBalMaxBlocks = 592;  // 4 per SM
+constexpr int kBalPer = 8;          // experts per lane: E <= 256
+constexpr int kBalStarts = 2048;    // sequence borders held in shared memory, else searched in global
+constexpr int kBalHist = 4096;      // (sequence, expert) counters of a block's tokens
+constexpr int kBalSpan = 512;       // and sequences
 constexpr double kBalFix = 4294967296.0;  // 2^32
-
-MOE_DEVICE float bal_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-MOE_DEVICE float bal_max(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
 
 // Scratch of a call, laid out by balance_layout.
 struct BalScratch {
-    int* status;
+    int* status;              // flags
+    int* bar;                 // grid barrier: arrivals, generation (left as found: zero, and any)
     int* done;                // blocks that have finished
     int* used;                // S': sequences with a counted token
     unsigned long long* all;  // N: counted tokens
@@ -60,170 +62,358 @@ struct BalArgs {
     float* losses;
     float* seq_loss;
     float* dlogits;
-    int64_t T;
+    int64_t T, chunk;  // tokens, tokens per block
     int E, K, S, sigmoid;
     float c_balance, c_z;
     BalScratch w;
 };
 
-// The sequence a token counts in, or -1.
-MOE_DEVICE int bal_sequence(const BalArgs& a, int64_t t)
+struct BalShared {
+    int starts[kBalStarts];
+    int hist[kBalHist];
+    int tokens[kBalSpan];
+    double red[2][kBalThreads / 32];
+    int lo, hi, last, gen;
+};
+
+// Largest i in 0 .. S with starts[i] <= t (0 when there is none).
+MOE_DEVICE int bal_find(const int32_t* starts, int S, int64_t t)
 {
-    int lo = 0, hi = a.S;  // largest i with starts[i] <= t
+    int lo = 0, hi = S;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)a.starts[mid] <= t) lo = mid;
+        if ((int64_t)starts[mid] <= t) lo = mid;
         else hi = mid - 1;
     }
-    if (lo >= a.S || (int64_t)a.starts[lo] > t || (int64_t)a.starts[lo + 1] <= t) return -1;
-    return a.mask == nullptr || a.mask[t] != 0 ? lo : -1;
+    return lo;
 }
 
-__global__ void __launch_bounds__(256) balance_zero_kernel(BalArgs a)
+// The sequence a token counts in, or -1.
+MOE_DEVICE int bal_sequence(const BalArgs& a, const int32_t* starts, int64_t t)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t step = (int64_t)gridDim.x * 256;
-    if (i == 0) {
+    const int i = bal_find(starts, a.S, t);
+    if (i >= a.S || (int64_t)starts[i] > t || (int64_t)starts[i + 1] <= t) return -1;
+    return a.mask == nullptr || a.mask[t] != 0 ? i : -1;
+}
+
+// The grid barrier in two halves.  Every thread calls both; the generation the
+// block waits out is kept in shared memory.
+MOE_DEVICE void bal_arrive(const BalArgs& a, BalShared& sh)
+{
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sh.gen = *(volatile int*)(a.w.bar + 1);
+        __threadfence();
+        if (atomicAdd(a.w.bar, 1) == (int)gridDim.x - 1) {
+            atomicExch(a.w.bar, 0);
+            __threadfence();
+            atomicAdd(a.w.bar + 1, 1);
+        }
+    }
+}
+
+// Bounded: after kWaitLimitNs the timeout flag is raised and the block goes on
+// (its results are then flagged as invalid).
+MOE_DEVICE void bal_wait(const BalArgs& a, BalShared& sh)
+{
+    if (threadIdx.x == 0) {
+        const int gen = sh.gen;
+        uint32_t spins = 0;
+        uint64_t t0 = 0;
+        while (*(volatile int*)(a.w.bar + 1) == gen) {
+            if ((++spins & 1023u) == 0u) {
+                if (t0 == 0) t0 = globaltimer_ns();
+                else if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    raise_flag(a.w.status, kFlagTimeout, 712);
+                    break;
+                }
+            }
+        }
+        __threadfence();
+    }
+    __syncthreads();
+}
+
+template <int L> MOE_DEVICE float group_sum(float v)
+{
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int L> MOE_DEVICE float group_max(float v)
+{
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// A lane's experts: 8 consecutive ones (rows of a multiple of 4: two 16-byte
+// vectors), or every L-th.
+template <int L, bool VEC> MOE_DEVICE int bal_expert(int lg, int j) { return VEC ? lg * kBalPer + j : lg + L * j; }
+
+template <int L, bool VEC, typename V>
+MOE_DEVICE void bal_load(const V* row, int lg, int E, V (&v)[kBalPer], V pad)
+{
+    if (VEC) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int e = lg * kBalPer + 4 * q;
+            if (e < E) {
+                const int4 w = __ldcg(reinterpret_cast<const int4*>(row + e));
+                const int x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * q + i] = *reinterpret_cast<const V*>(&x[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * q + i] = pad;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kBalPer; ++j) {
+            const int e = lg + L * j;
+            v[j] = e < E ? __ldcg(row + e) : pad;
+        }
+    }
+}
+
+template <int L, bool VEC>
+MOE_DEVICE void bal_store(float* row, int lg, int E, const float (&v)[kBalPer])
+{
+    if (VEC) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int e = lg * kBalPer + 4 * q;
+            if (e < E)
+                *reinterpret_cast<float4*>(row + e) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kBalPer; ++j) {
+            const int e = lg + L * j;
+            if (e < E) row[e] = v[j];
+        }
+    }
+}
+
+template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) balance_kernel(const BalArgs a)
+{
+    __shared__ BalShared sh;
+    const int tid = threadIdx.x, E = a.E;
+    const int64_t gtid = (int64_t)blockIdx.x * kBalThreads + tid, gstep = (int64_t)gridDim.x * kBalThreads;
+    const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = t0 + a.chunk < a.T ? t0 + a.chunk : a.T;
+    // zero this call's sums; check the borders
+    if (gtid == 0) {
         *a.w.done = 0;
         *a.w.used = 0;
         *a.w.all = 0;
     }
-    for (int64_t k = i; k < a.S; k += step) {
+    for (int64_t k = gtid; k < a.S; k += gstep) {
         a.w.tokens[k] = 0;
         a.w.bad[k] = 0;
         a.w.acc[k] = 0;
         const int64_t b0 = a.starts[k], b1 = a.starts[k + 1];
         if (b0 < 0 || b1 < b0 || b1 > a.T) raise_flag(a.w.status, kFlagBounds, 710);
     }
-    for (int64_t k = i; k < (int64_t)a.S * a.E; k += step) a.counts[k] = 0;
-}
+    for (int64_t k = gtid; k < (int64_t)a.S * E; k += gstep) a.counts[k] = 0;
+    bal_arrive(a, sh);
 
-__global__ void __launch_bounds__(256) balance_count_kernel(BalArgs a)
-{
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= a.T) return;
-    const int i = bal_sequence(a, t);
-    if (i < 0) return;
-    if (atomicAdd(&a.w.tokens[i], 1) == 0) atomicAdd(a.w.used, 1);
-    atomicAdd(a.w.all, 1ull);
-    for (int k = 0; k < a.K; ++k) {
-        const int id = a.ids[t * a.K + k];
-        if (id < 0 || id >= a.E) raise_flag(a.w.status, kFlagBounds, 711);
-        else atomicAdd(&a.counts[(int64_t)i * a.E + id], 1);
+    // this block's counts, in shared memory where its tokens' sequences fit
+    const int32_t* starts = a.starts;
+    if (a.S < kBalStarts) {
+        for (int i = tid; i <= a.S; i += kBalThreads) sh.starts[i] = a.starts[i];
+        starts = sh.starts;
     }
-}
+    for (int i = tid; i < kBalHist; i += kBalThreads) sh.hist[i] = 0;
+    for (int i = tid; i < kBalSpan; i += kBalThreads) sh.tokens[i] = 0;
+    __syncthreads();
+    if (tid == 0) sh.lo = bal_find(starts, a.S, t0);
+    if (tid == 32) sh.hi = bal_find(starts, a.S, t1 - 1);
+    __syncthreads();
+    const int lo = sh.lo, span = sh.hi - lo + 1;
+    const bool local = span >= 1 && span <= kBalSpan && (int64_t)span * E <= kBalHist;
+    auto count = [&](bool in_shared) {
+        for (int64_t t = t0 + tid; t < t1; t += kBalThreads) {
+            const int i = bal_sequence(a, starts, t);
+            if (i < 0) continue;
+            const bool here = in_shared && i >= lo && i < lo + span;
+            if (here) {
+                atomicAdd(&sh.tokens[i - lo], 1);
+            } else {
+                if (atomicAdd(&a.w.tokens[i], 1) == 0) atomicAdd(a.w.used, 1);
+                atomicAdd(a.w.all, 1ull);
+            }
+            for (int k = 0; k < a.K; ++k) {
+                const int id = a.ids[t * a.K + k];
+                if (id < 0 || id >= E) raise_flag(a.w.status, kFlagBounds, 711);
+                else if (here) atomicAdd(&sh.hist[(i - lo) * E + id], 1);
+                else atomicAdd(&a.counts[(int64_t)i * E + id], 1);
+            }
+        }
+    };
+    // borders that do not rise can put a token outside lo .. hi: those blocks count
+    // in global memory like the ones whose sequences do not fit
+    bool rising = true;
+    if (local)
+        for (int i = lo + tid; i < lo + span && i < a.S; i += kBalThreads) rising &= starts[i] <= starts[i + 1];
+    const bool in_shared = __syncthreads_and(local && rising) != 0;
+    if (in_shared) count(true);
+    bal_wait(a, sh);  // the sums are zero everywhere
+    if (in_shared) {
+        for (int i = tid; i < span && lo + i < a.S; i += kBalThreads) {
+            const int n = sh.tokens[i];
+            if (n > 0) {
+                if (atomicAdd(&a.w.tokens[lo + i], n) == 0) atomicAdd(a.w.used, 1);
+                atomicAdd(a.w.all, (unsigned long long)n);
+            }
+        }
+        for (int i = tid; i < span * E; i += kBalThreads) {
+            const int n = sh.hist[i];
+            if (n > 0) atomicAdd(&a.counts[(int64_t)lo * E + i], n);
+        }
+    } else {
+        count(false);
+    }
+    bal_arrive(a, sh);
 
-__global__ void __launch_bounds__(256) balance_grad_kernel(BalArgs a)
-{
-    __shared__ double zs[8];
-    __shared__ int last;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int E = a.E;
-    const float total = (float)*a.w.all, used = (float)*a.w.used;
-    double z = 0.0;
-    for (int n = 0; n < kBalTokens / 8; ++n) {
-        const int64_t t = (int64_t)blockIdx.x * kBalTokens + n * 8 + warp;
-        if (t >= a.T) break;
-        const int i = bal_sequence(a, t);
-        float* out = a.dlogits != nullptr ? a.dlogits + t * E : nullptr;
-        if (i < 0) {
-            if (out != nullptr)
-                for (int e = lane; e < E; e += 32) out[e] = 0.f;
-            continue;
-        }
-        const float* L = a.logits + t * E;
-        float l[kBalPerLane], p[kBalPerLane];
+    // the tokens, kBalThreads / L at a time; the first ones' softmax before the wait
+    const int lg = tid & (L - 1);
+    const int64_t per = kBalThreads / L;
+    float l[kBalPer], p[kBalPer], f[kBalPer];
+    float lse = 0.f, se = 1.f, sg = 1.f;
+    int i = -1, i_of = -1;  // the token's sequence; the one f is of
+    auto softmax = [&](int64_t t) {  // p = exp(l - max); for sigmoid scores, l becomes the score
+        i = t < t1 ? bal_sequence(a, starts, t) : -1;
         float mx = -INFINITY;
+        if (i >= 0) {
+            bal_load<L, VEC, float>(a.logits + t * E, lg, E, l, -INFINITY);
 #pragma unroll
-        for (int j = 0; j < kBalPerLane; ++j) {
-            const int e = lane + 32 * j;
-            l[j] = e < E ? L[e] : -INFINITY;
-            mx = fmaxf(mx, l[j]);
+            for (int j = 0; j < kBalPer; ++j) mx = fmaxf(mx, l[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kBalPer; ++j) l[j] = 0.f;
         }
-        mx = bal_max(mx);
-        float se = 0.f, sg = 0.f;
+        mx = group_max<L>(mx);
+        se = 0.f;
+        sg = 0.f;
 #pragma unroll
-        for (int j = 0; j < kBalPerLane; ++j) {
-            const bool in = lane + 32 * j < E;
+        for (int j = 0; j < kBalPer; ++j) {
+            const bool in = bal_expert<L, VEC>(lg, j) < E;
             p[j] = in ? expf(l[j] - mx) : 0.f;
             se += p[j];
             if (a.sigmoid) {
-                l[j] = in ? 1.f / (1.f + expf(-l[j])) : 0.f;  // the score
+                l[j] = in ? 1.f / (1.f + expf(-l[j])) : 0.f;
                 sg += l[j];
             }
         }
-        se = bal_sum(se);
-        if (a.sigmoid) sg = bal_sum(sg);
-        const float lse = mx + logf(se);
-        const float inv_n = 1.f / (float)a.w.tokens[i];
-        const float fscale = inv_n / (float)a.K;
-        const int32_t* cnt = a.counts + (int64_t)i * E;
-        float f[kBalPerLane], c = 0.f;
+        se = group_sum<L>(se);
+        if (a.sigmoid) sg = group_sum<L>(sg);
+        lse = mx + logf(se);
+    };
+    softmax(t0 + tid / L);
+    bal_wait(a, sh);  // the counts are complete
+    const float total = (float)__ldcg(a.w.all), used = (float)__ldcg(a.w.used);
+    float inv_n = 0.f;
+    unsigned long long acc = 0;  // of sequence i_of
+    double z = 0.0;
+    for (int64_t base = t0; base < t1; base += per) {
+        const int64_t t = base + tid / L;
+        if (base != t0) softmax(t);
+        float c = 0.f;
+        if (i >= 0) {
+            if (i != i_of) {
+                if (acc != 0 && lg == 0) atomicAdd(&a.w.acc[i_of], acc);
+                acc = 0;
+                i_of = i;
+                inv_n = 1.f / (float)__ldcg(&a.w.tokens[i]);
+                const float fscale = inv_n / (float)a.K;
+                int n[kBalPer];
+                bal_load<L, VEC, int>(a.counts + (int64_t)i * E, lg, E, n, 0);
 #pragma unroll
-        for (int j = 0; j < kBalPerLane; ++j) {
-            const int e = lane + 32 * j;
-            f[j] = e < E ? (float)cnt[e] * fscale : 0.f;
-            c += f[j] * (a.sigmoid ? l[j] / sg : p[j] / se);
-        }
-        c = bal_sum(c);
-        z += (double)lse * (double)lse;
-        if (lane == 0) {
-            if (c >= 0.f && c <= 1.5f)
-                atomicAdd(&a.w.acc[i], (unsigned long long)((double)c * kBalFix + 0.5));
-            else
-                a.w.bad[i] = 1;
-        }
-        if (out != nullptr) {
-            const float cb = a.c_balance * (float)E / used * inv_n, cz = a.c_z * 2.f * lse / total;
-#pragma unroll
-            for (int j = 0; j < kBalPerLane; ++j) {
-                const int e = lane + 32 * j;
-                if (e >= E) continue;
-                const float soft = p[j] / se;
-                const float dp = a.sigmoid ? l[j] / sg * (1.f - l[j]) : soft;
-                out[e] = cb * dp * (f[j] - c) + cz * soft;
+                for (int j = 0; j < kBalPer; ++j) f[j] = (float)n[j] * fscale;
             }
+#pragma unroll
+            for (int j = 0; j < kBalPer; ++j) c += f[j] * (a.sigmoid ? l[j] / sg : p[j] / se);
+        }
+        c = group_sum<L>(c);
+        if (t < t1 && (i >= 0 || a.dlogits != nullptr)) {
+            float d[kBalPer];
+            if (i >= 0) {
+                if (lg == 0) {
+                    z += (double)lse * (double)lse;
+                    if (c >= 0.f && c <= 1.5f) acc += (unsigned long long)((double)c * kBalFix + 0.5);
+                    else a.w.bad[i] = 1;
+                }
+                const float cb = a.c_balance * (float)E / used * inv_n, cz = a.c_z * 2.f * lse / total;
+#pragma unroll
+                for (int j = 0; j < kBalPer; ++j) {
+                    const float soft = p[j] / se;
+                    const float dp = a.sigmoid ? l[j] / sg * (1.f - l[j]) : soft;
+                    d[j] = cb * dp * (f[j] - c) + cz * soft;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kBalPer; ++j) d[j] = 0.f;
+            }
+            if (a.dlogits != nullptr) bal_store<L, VEC>(a.dlogits + t * E, lg, E, d);
         }
     }
-    if (lane == 0) zs[warp] = z;
+    // the warp's shares of one sequence as one addition
+    const int i0 = __shfl_sync(0xffffffffu, i_of, 0);
+    if (__all_sync(0xffffffffu, i_of == i0 || acc == 0)) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+        if ((tid & 31) == 0 && acc != 0) atomicAdd(&a.w.acc[i0], acc);
+    } else if (acc != 0) {
+        atomicAdd(&a.w.acc[i_of], acc);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if ((tid & 31) == 0) sh.red[0][tid >> 5] = z;
+    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         double s = 0.0;
-        for (int w = 0; w < 8; ++w) s += zs[w];
+        for (int w = 0; w < kBalThreads / 32; ++w) s += sh.red[0][w];
         a.w.zpart[blockIdx.x] = s;
         __threadfence();
-        last = atomicAdd(a.w.done, 1) == (int)gridDim.x - 1;
+        sh.last = atomicAdd(a.w.done, 1) == (int)gridDim.x - 1;
     }
     __syncthreads();
-    if (!last) return;
+    if (!sh.last) return;
     __threadfence();
     // the block that finishes last: per-sequence losses, then both means
-    __shared__ double red[2][256];
     double zsum = 0.0, bsum = 0.0;
-    for (int64_t b = threadIdx.x; b < gridDim.x; b += 256) zsum += __ldcg(&a.w.zpart[b]);
-    for (int64_t i = threadIdx.x; i < a.S; i += 256) {
-        const int n = __ldcg(&a.w.tokens[i]);
-        double L = 0.0;
+    for (int64_t b = tid; b < gridDim.x; b += kBalThreads) zsum += __ldcg(&a.w.zpart[b]);
+    for (int64_t k = tid; k < a.S; k += kBalThreads) {
+        const int n = __ldcg(&a.w.tokens[k]);
+        double v = 0.0;
         if (n > 0)
-            L = __ldcg(&a.w.bad[i]) ? (double)NAN : (double)E * ((double)__ldcg(&a.w.acc[i]) / kBalFix) / (double)n;
-        a.seq_loss[i] = (float)L;
-        bsum += L;
+            v = __ldcg(&a.w.bad[k]) ? (double)NAN : (double)E * ((double)__ldcg(&a.w.acc[k]) / kBalFix) / (double)n;
+        a.seq_loss[k] = (float)v;
+        bsum += v;
     }
-    red[0][threadIdx.x] = zsum;
-    red[1][threadIdx.x] = bsum;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        zsum += __shfl_xor_sync(0xffffffffu, zsum, o);
+        bsum += __shfl_xor_sync(0xffffffffu, bsum, o);
+    }
+    if ((tid & 31) == 0) {
+        sh.red[0][tid >> 5] = zsum;
+        sh.red[1][tid >> 5] = bsum;
+    }
     __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-        if ((int)threadIdx.x < o) {
-            red[0][threadIdx.x] += red[0][threadIdx.x + o];
-            red[1][threadIdx.x] += red[1][threadIdx.x + o];
+    if (tid == 0) {
+        double zt = 0.0, bt = 0.0;
+        for (int w = 0; w < kBalThreads / 32; ++w) {
+            zt += sh.red[0][w];
+            bt += sh.red[1][w];
         }
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) {
         const unsigned long long all = __ldcg(a.w.all);
         const int u = __ldcg(a.w.used);
-        a.losses[0] = all ? (float)(red[0][0] / (double)all) : 0.f;
-        a.losses[1] = u ? (float)(red[1][0] / (double)u) : 0.f;
+        a.losses[0] = all ? (float)(zt / (double)all) : 0.f;
+        a.losses[1] = u ? (float)(bt / (double)u) : 0.f;
     }
 }
 
@@ -231,50 +421,78 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(BalArgs a)
 struct BalLayout {
     size_t head, tokens, bad, acc, zpart, total;
 };
-static int64_t bal_blocks(const moe_config& c) { return (c.T + kBalTokens - 1) / kBalTokens; }
-static BalLayout balance_layout(const moe_config& c, int64_t S)
+static BalLayout balance_layout(int64_t S)
 {
     BalLayout L;
     size_t o = 0;
-    L.head = o;   o += 256;  // status word, then at 64 bytes the call's counters
+    L.head = o;   o += 256;  // status word, then the call's counters
     L.tokens = o; o += align_up((size_t)S * 4);
     L.bad = o;    o += align_up((size_t)S * 4);
     L.acc = o;    o += align_up((size_t)S * 8);
-    L.zpart = o;  o += align_up((size_t)bal_blocks(c) * 8);
+    L.zpart = o;  o += align_up((size_t)kBalMaxBlocks * 8);
     L.total = o;
     return L;
 }
-size_t balance_bytes(const moe_config& c, int64_t S) { return balance_layout(c, S).total; }
+size_t balance_bytes(const moe_config&, int64_t S) { return balance_layout(S).total; }
+
+template <int L, bool VEC> static cudaError_t launch_balance_t(BalArgs a, cudaStream_t s)
+{
+    // resident blocks, per device (the launch is cooperative)
+    static std::atomic<int> cached[32];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int resident = dev >= 0 && dev < 32 ? cached[dev].load(std::memory_order_acquire) : 0;
+    if (resident == 0) {
+        int per_sm = 0, sms = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, balance_kernel<L, VEC>, kBalThreads, 0);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        resident = per_sm * sms;
+        if (resident < 1) return cudaErrorInvalidConfiguration;
+        if (dev >= 0 && dev < 32) cached[dev].store(resident, std::memory_order_release);
+    }
+    int64_t blocks = (a.T * L + kBalThreads - 1) / kBalThreads;
+    if (blocks > resident) blocks = resident;
+    if (blocks > kBalMaxBlocks) blocks = kBalMaxBlocks;
+    a.chunk = (a.T + blocks - 1) / blocks;
+    blocks = (a.T + a.chunk - 1) / a.chunk;  // none without tokens
+    void* args[] = {&a};
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(balance_kernel<L, VEC>), dim3((unsigned)blocks),
+                                       dim3(kBalThreads), args, 0, s);
+}
+
+template <int L> static cudaError_t launch_balance_l(const BalArgs& a, cudaStream_t s)
+{
+    return a.E % 4 == 0 ? launch_balance_t<L, true>(a, s) : launch_balance_t<L, false>(a, s);
+}
 
 cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, const int32_t* ids,
                            const int32_t* starts, const uint8_t* mask, float c_balance, float c_z, int32_t* counts,
                            float* losses, float* seq_loss, float* dlogits, void* ws, cudaStream_t s)
 {
-    const BalLayout L = balance_layout(c, S);
+    const BalLayout L = balance_layout(S);
     char* w = static_cast<char*>(ws);
     BalArgs a;
     a.logits = logits; a.ids = ids; a.starts = starts; a.mask = mask;
     a.counts = counts; a.losses = losses; a.seq_loss = seq_loss; a.dlogits = dlogits;
-    a.T = c.T; a.E = c.E; a.K = c.K; a.S = (int)S; a.sigmoid = c.score_func == MOE_SCORE_SIGMOID;
+    a.T = c.T; a.chunk = 0; a.E = c.E; a.K = c.K; a.S = (int)S; a.sigmoid = c.score_func == MOE_SCORE_SIGMOID;
     a.c_balance = c_balance; a.c_z = c_z;
     a.w.status = reinterpret_cast<int*>(w + L.head);
-    a.w.done = reinterpret_cast<int*>(w + L.head + 64);
-    a.w.used = reinterpret_cast<int*>(w + L.head + 68);
-    a.w.all = reinterpret_cast<unsigned long long*>(w + L.head + 72);
+    a.w.bar = reinterpret_cast<int*>(w + L.head + 64);
+    a.w.done = reinterpret_cast<int*>(w + L.head + 80);
+    a.w.used = reinterpret_cast<int*>(w + L.head + 84);
+    a.w.all = reinterpret_cast<unsigned long long*>(w + L.head + 88);
     a.w.tokens = reinterpret_cast<int*>(w + L.tokens);
     a.w.bad = reinterpret_cast<int*>(w + L.bad);
     a.w.acc = reinterpret_cast<unsigned long long*>(w + L.acc);
     a.w.zpart = reinterpret_cast<double*>(w + L.zpart);
-    int64_t zb = (S * c.E + 255) / 256;
-    if (zb > 148) zb = 148;
-    balance_zero_kernel<<<(unsigned)zb, 256, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    balance_count_kernel<<<(unsigned)((c.T + 255) / 256), 256, 0, s>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    balance_grad_kernel<<<(unsigned)bal_blocks(c), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    if (c.E <= 8) return launch_balance_l<1>(a, s);
+    if (c.E <= 16) return launch_balance_l<2>(a, s);
+    if (c.E <= 32) return launch_balance_l<4>(a, s);
+    if (c.E <= 64) return launch_balance_l<8>(a, s);
+    if (c.E <= 128) return launch_balance_l<16>(a, s);
+    return launch_balance_l<32>(a, s);
 }
 
 }  // namespace moe

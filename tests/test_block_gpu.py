@@ -354,7 +354,7 @@ def test_balance_faults_are_seen():
         _, ws = _balance(logits, ids, starts)
         assert B.moe_get_device_status(ws) == B.MOE_DEVFLAG_BOUNDS
         B.moe_clear_device_status(ws)
-        _, ws = _balance(logits, ids, [0, 20, 32], ws=torch.zeros(4096, dtype=torch.uint8, device="cuda"))
+        _, ws = _balance(logits, ids, [0, 20, 32])
         assert B.moe_get_device_status(ws) == 0
     for bad in (-1, 8):
         i2 = ids.clone()
