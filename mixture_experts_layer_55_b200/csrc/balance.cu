@@ -43,10 +43,8 @@ constexpr double kBalFix = 4294967296.0;  // 2^32
 // Scratch of a call, laid out by balance_layout.
 struct BalScratch {
     int* status;              // flags
-    int* bar;                 // grid barrier: arrivals, generation (left as found: zero, and any)
-    int* done;                // blocks that have finished
-    int* used;                // S': sequences with a counted token
-    unsigned long long* all;  // N: counted tokens
+    uint32_t* bar;            // grid barrier: arrivals (zero between calls)
+    uint32_t* done;           // blocks that have finished (zero between calls)
     int* tokens;              // (S) n_i
     int* bad;                 // (S) a counted token's c_t is not a number
     unsigned long long* acc;  // (S) sum of c_t in 2^-32
@@ -73,7 +71,9 @@ struct BalShared {
     int hist[kBalHist];
     int tokens[kBalSpan];
     double red[2][kBalThreads / 32];
-    int lo, hi, last, gen;
+    unsigned long long all[kBalThreads / 32];
+    int used[kBalThreads / 32];
+    int lo, hi, last;
 };
 
 // Largest i in 0 .. S with starts[i] <= t (0 when there is none).
@@ -96,32 +96,26 @@ MOE_DEVICE int bal_sequence(const BalArgs& a, const int32_t* starts, int64_t t)
     return a.mask == nullptr || a.mask[t] != 0 ? i : -1;
 }
 
-// The grid barrier in two halves.  Every thread calls both; the generation the
-// block waits out is kept in shared memory.
-MOE_DEVICE void bal_arrive(const BalArgs& a, BalShared& sh)
+// The grid barrier in two halves: a count of arrivals that only grows within a
+// call (the block that finishes last sets it back to zero).  Thread 0's release
+// covers what the block's other threads wrote before the block barrier.
+MOE_DEVICE void bal_arrive(const BalArgs& a)
 {
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) {
-        sh.gen = *(volatile int*)(a.w.bar + 1);
-        __threadfence();
-        if (atomicAdd(a.w.bar, 1) == (int)gridDim.x - 1) {
-            atomicExch(a.w.bar, 0);
-            __threadfence();
-            atomicAdd(a.w.bar + 1, 1);
-        }
-    }
+    if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.w.bar) : "memory");
 }
 
-// Bounded: after kWaitLimitNs the timeout flag is raised and the block goes on
-// (its results are then flagged as invalid).
-MOE_DEVICE void bal_wait(const BalArgs& a, BalShared& sh)
+// Waits for the n-th arrival of every block.  Bounded: after kWaitLimitNs the
+// timeout flag is raised and the block goes on (its results are then flagged as
+// invalid).
+MOE_DEVICE void bal_wait(const BalArgs& a, uint32_t n)
 {
     if (threadIdx.x == 0) {
-        const int gen = sh.gen;
-        uint32_t spins = 0;
+        uint32_t spins = 0, v;
         uint64_t t0 = 0;
-        while (*(volatile int*)(a.w.bar + 1) == gen) {
+        while (true) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.w.bar) : "memory");
+            if (v >= n * gridDim.x) break;
             if ((++spins & 1023u) == 0u) {
                 if (t0 == 0) t0 = globaltimer_ns();
                 else if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -130,7 +124,6 @@ MOE_DEVICE void bal_wait(const BalArgs& a, BalShared& sh)
                 }
             }
         }
-        __threadfence();
     }
     __syncthreads();
 }
@@ -203,21 +196,18 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
     const int tid = threadIdx.x, E = a.E;
     const int64_t gtid = (int64_t)blockIdx.x * kBalThreads + tid, gstep = (int64_t)gridDim.x * kBalThreads;
     const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = t0 + a.chunk < a.T ? t0 + a.chunk : a.T;
-    // zero this call's sums; check the borders
-    if (gtid == 0) {
-        *a.w.done = 0;
-        *a.w.used = 0;
-        *a.w.all = 0;
-    }
+    // zero this call's sums, then check the borders
     for (int64_t k = gtid; k < a.S; k += gstep) {
         a.w.tokens[k] = 0;
         a.w.bad[k] = 0;
         a.w.acc[k] = 0;
+    }
+    for (int64_t k = gtid; k < (int64_t)a.S * E; k += gstep) a.counts[k] = 0;
+    bal_arrive(a);
+    for (int64_t k = gtid; k < a.S; k += gstep) {
         const int64_t b0 = a.starts[k], b1 = a.starts[k + 1];
         if (b0 < 0 || b1 < b0 || b1 > a.T) raise_flag(a.w.status, kFlagBounds, 710);
     }
-    for (int64_t k = gtid; k < (int64_t)a.S * E; k += gstep) a.counts[k] = 0;
-    bal_arrive(a, sh);
 
     // this block's counts, in shared memory where its tokens' sequences fit
     const int32_t* starts = a.starts;
@@ -235,20 +225,19 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
     const bool local = span >= 1 && span <= kBalSpan && (int64_t)span * E <= kBalHist;
     auto count = [&](bool in_shared) {
         for (int64_t t = t0 + tid; t < t1; t += kBalThreads) {
+            int id[8];  // K <= 8; on their way while the sequence is looked up
+#pragma unroll
+            for (int k = 0; k < 8; ++k) id[k] = k < a.K ? a.ids[t * a.K + k] : 0;
             const int i = bal_sequence(a, starts, t);
             if (i < 0) continue;
             const bool here = in_shared && i >= lo && i < lo + span;
-            if (here) {
-                atomicAdd(&sh.tokens[i - lo], 1);
-            } else {
-                if (atomicAdd(&a.w.tokens[i], 1) == 0) atomicAdd(a.w.used, 1);
-                atomicAdd(a.w.all, 1ull);
-            }
-            for (int k = 0; k < a.K; ++k) {
-                const int id = a.ids[t * a.K + k];
-                if (id < 0 || id >= E) raise_flag(a.w.status, kFlagBounds, 711);
-                else if (here) atomicAdd(&sh.hist[(i - lo) * E + id], 1);
-                else atomicAdd(&a.counts[(int64_t)i * E + id], 1);
+            atomicAdd(here ? &sh.tokens[i - lo] : &a.w.tokens[i], 1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (k >= a.K) break;
+                if (id[k] < 0 || id[k] >= E) raise_flag(a.w.status, kFlagBounds, 711);
+                else if (here) atomicAdd(&sh.hist[(i - lo) * E + id[k]], 1);
+                else atomicAdd(&a.counts[(int64_t)i * E + id[k]], 1);
             }
         }
     };
@@ -259,14 +248,11 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
         for (int i = lo + tid; i < lo + span && i < a.S; i += kBalThreads) rising &= starts[i] <= starts[i + 1];
     const bool in_shared = __syncthreads_and(local && rising) != 0;
     if (in_shared) count(true);
-    bal_wait(a, sh);  // the sums are zero everywhere
+    bal_wait(a, 1);  // the sums are zero everywhere
     if (in_shared) {
         for (int i = tid; i < span && lo + i < a.S; i += kBalThreads) {
             const int n = sh.tokens[i];
-            if (n > 0) {
-                if (atomicAdd(&a.w.tokens[lo + i], n) == 0) atomicAdd(a.w.used, 1);
-                atomicAdd(a.w.all, (unsigned long long)n);
-            }
+            if (n > 0) atomicAdd(&a.w.tokens[lo + i], n);
         }
         for (int i = tid; i < span * E; i += kBalThreads) {
             const int n = sh.hist[i];
@@ -275,88 +261,123 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
     } else {
         count(false);
     }
-    bal_arrive(a, sh);
+    bal_arrive(a);
 
-    // the tokens, kBalThreads / L at a time; the first ones' softmax before the wait
+    // the tokens, kBalThreads / L at a time, the next one's logits loaded while one
+    // is worked on (the first one's before the wait)
     const int lg = tid & (L - 1);
     const int64_t per = kBalThreads / L;
-    float l[kBalPer], p[kBalPer], f[kBalPer];
-    float lse = 0.f, se = 1.f, sg = 1.f;
-    int i = -1, i_of = -1;  // the token's sequence; the one f is of
-    auto softmax = [&](int64_t t) {  // p = exp(l - max); for sigmoid scores, l becomes the score
-        i = t < t1 ? bal_sequence(a, starts, t) : -1;
-        float mx = -INFINITY;
-        if (i >= 0) {
-            bal_load<L, VEC, float>(a.logits + t * E, lg, E, l, -INFINITY);
-#pragma unroll
-            for (int j = 0; j < kBalPer; ++j) mx = fmaxf(mx, l[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kBalPer; ++j) l[j] = 0.f;
+    float nl[kBalPer], f[kBalPer];
+    int ni = -1, at = -1, i_of = -1;  // the next token's sequence; where it was found; the one f is of
+    auto fetch = [&](int64_t t) {
+        ni = -1;
+        if (t >= t1) return;
+        const bool on = a.mask == nullptr || a.mask[t] != 0;
+        bal_load<L, VEC, float>(a.logits + t * E, lg, E, nl, -INFINITY);  // (not used where the token does not count)
+        if (at < 0 || (int64_t)starts[at] > t || (int64_t)starts[at + 1] <= t) {  // most tokens stay in a sequence
+            at = bal_find(starts, a.S, t);
+            if (at >= a.S || (int64_t)starts[at] > t || (int64_t)starts[at + 1] <= t) at = -1;
         }
-        mx = group_max<L>(mx);
-        se = 0.f;
-        sg = 0.f;
-#pragma unroll
-        for (int j = 0; j < kBalPer; ++j) {
-            const bool in = bal_expert<L, VEC>(lg, j) < E;
-            p[j] = in ? expf(l[j] - mx) : 0.f;
-            se += p[j];
-            if (a.sigmoid) {
-                l[j] = in ? 1.f / (1.f + expf(-l[j])) : 0.f;
-                sg += l[j];
-            }
-        }
-        se = group_sum<L>(se);
-        if (a.sigmoid) sg = group_sum<L>(sg);
-        lse = mx + logf(se);
+        if (on) ni = at;
     };
-    softmax(t0 + tid / L);
-    bal_wait(a, sh);  // the counts are complete
-    const float total = (float)__ldcg(a.w.all), used = (float)__ldcg(a.w.used);
+    fetch(t0 + tid / L);
+    bal_wait(a, 2);  // the counts are complete
+    // S' and N
+    int my_used = 0;
+    unsigned long long my_all = 0;
+    for (int k = tid; k < a.S; k += kBalThreads) {
+        const int n = __ldcg(&a.w.tokens[k]);
+        my_used += n > 0;
+        my_all += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        my_used += __shfl_xor_sync(0xffffffffu, my_used, o);
+        my_all += __shfl_xor_sync(0xffffffffu, my_all, o);
+    }
+    if ((tid & 31) == 0) {
+        sh.used[tid >> 5] = my_used;
+        sh.all[tid >> 5] = my_all;
+    }
+    __syncthreads();
+    int used = 0;
+    unsigned long long all = 0;
+    for (int w = 0; w < kBalThreads / 32; ++w) {
+        used += sh.used[w];
+        all += sh.all[w];
+    }
+    const float cb0 = a.c_balance * (float)E / (float)used, cz0 = a.c_z * 2.f / (float)all;
     float inv_n = 0.f;
     unsigned long long acc = 0;  // of sequence i_of
     double z = 0.0;
     for (int64_t base = t0; base < t1; base += per) {
         const int64_t t = base + tid / L;
-        if (base != t0) softmax(t);
-        float c = 0.f;
-        if (i >= 0) {
-            if (i != i_of) {
-                if (acc != 0 && lg == 0) atomicAdd(&a.w.acc[i_of], acc);
-                acc = 0;
-                i_of = i;
-                inv_n = 1.f / (float)__ldcg(&a.w.tokens[i]);
-                const float fscale = inv_n / (float)a.K;
-                int n[kBalPer];
-                bal_load<L, VEC, int>(a.counts + (int64_t)i * E, lg, E, n, 0);
+        const int i = ni;
+        float l[kBalPer], p[kBalPer];
+        float mx = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < kBalPer; ++j) f[j] = (float)n[j] * fscale;
+        for (int j = 0; j < kBalPer; ++j) {
+            l[j] = i >= 0 ? nl[j] : 0.f;
+            mx = fmaxf(mx, l[j]);
+        }
+        if (base + per < t1) fetch(t + per);
+        if (i >= 0 && i != i_of) {
+            if (acc != 0) atomicAdd(&a.w.acc[i_of], acc);
+            acc = 0;
+            i_of = i;
+            inv_n = 1.f / (float)__ldcg(&a.w.tokens[i]);
+            const float fscale = inv_n / (float)a.K;
+            int n[kBalPer];
+            bal_load<L, VEC, int>(a.counts + (int64_t)i * E, lg, E, n, 0);
+#pragma unroll
+            for (int j = 0; j < kBalPer; ++j) f[j] = (float)n[j] * fscale;
+        }
+        // softmax: p = exp(l - max) / sum; sigmoid scores: l becomes score / sum of
+        // scores.  The fast exponential and reciprocal are good to 2^-22 and the
+        // rounding of their argument, |l - max| 2^-24, which the subtraction has too.
+        mx = group_max<L>(mx);
+        float se = 0.f, sg = 0.f, one_less[kBalPer];
+#pragma unroll
+        for (int j = 0; j < kBalPer; ++j) {
+            const bool in = bal_expert<L, VEC>(lg, j) < E;
+            p[j] = in ? __expf(l[j] - mx) : 0.f;
+            se += p[j];
+            if (a.sigmoid) {
+                const float sc = in ? __fdividef(1.f, 1.f + __expf(-l[j])) : 0.f;
+                l[j] = sc;
+                one_less[j] = 1.f - sc;
+                sg += sc;
             }
+        }
+        se = group_sum<L>(se);
+        const float lse = mx + logf(se), inv_se = __fdividef(1.f, se);
+        if (a.sigmoid) {
+            const float inv_sg = __fdividef(1.f, group_sum<L>(sg));
 #pragma unroll
-            for (int j = 0; j < kBalPer; ++j) c += f[j] * (a.sigmoid ? l[j] / sg : p[j] / se);
+            for (int j = 0; j < kBalPer; ++j) l[j] *= inv_sg;
+        }
+        float c = 0.f;
+#pragma unroll
+        for (int j = 0; j < kBalPer; ++j) {
+            p[j] *= inv_se;
+            c += i >= 0 ? f[j] * (a.sigmoid ? l[j] : p[j]) : 0.f;
         }
         c = group_sum<L>(c);
-        if (t < t1 && (i >= 0 || a.dlogits != nullptr)) {
+        if (t >= t1) continue;
+        if (i >= 0 && lg == 0) {
+            z = fma((double)lse, (double)lse, z);
+            if (c >= 0.f && c <= 1.5f) acc += __float2ull_rn(c * (float)kBalFix);  // exact but for the rounding
+            else a.w.bad[i] = 1;
+        }
+        if (a.dlogits != nullptr) {
             float d[kBalPer];
-            if (i >= 0) {
-                if (lg == 0) {
-                    z += (double)lse * (double)lse;
-                    if (c >= 0.f && c <= 1.5f) acc += (unsigned long long)((double)c * kBalFix + 0.5);
-                    else a.w.bad[i] = 1;
-                }
-                const float cb = a.c_balance * (float)E / used * inv_n, cz = a.c_z * 2.f * lse / total;
+            const float cb = cb0 * inv_n, cz = cz0 * lse;
 #pragma unroll
-                for (int j = 0; j < kBalPer; ++j) {
-                    const float soft = p[j] / se;
-                    const float dp = a.sigmoid ? l[j] / sg * (1.f - l[j]) : soft;
-                    d[j] = cb * dp * (f[j] - c) + cz * soft;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < kBalPer; ++j) d[j] = 0.f;
+            for (int j = 0; j < kBalPer; ++j) {
+                const float dp = a.sigmoid ? l[j] * one_less[j] : p[j];
+                d[j] = i >= 0 ? cb * dp * (f[j] - c) + cz * p[j] : 0.f;
             }
-            if (a.dlogits != nullptr) bal_store<L, VEC>(a.dlogits + t * E, lg, E, d);
+            bal_store<L, VEC>(a.dlogits + t * E, lg, E, d);
         }
     }
     // the warp's shares of one sequence as one addition
@@ -378,7 +399,7 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
         for (int w = 0; w < kBalThreads / 32; ++w) s += sh.red[0][w];
         a.w.zpart[blockIdx.x] = s;
         __threadfence();
-        sh.last = atomicAdd(a.w.done, 1) == (int)gridDim.x - 1;
+        sh.last = atomicAdd(a.w.done, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!sh.last) return;
@@ -405,15 +426,15 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
     }
     __syncthreads();
     if (tid == 0) {
+        *a.w.bar = 0;  // every block has passed both barriers
+        *a.w.done = 0;
         double zt = 0.0, bt = 0.0;
         for (int w = 0; w < kBalThreads / 32; ++w) {
             zt += sh.red[0][w];
             bt += sh.red[1][w];
         }
-        const unsigned long long all = __ldcg(a.w.all);
-        const int u = __ldcg(a.w.used);
         a.losses[0] = all ? (float)(zt / (double)all) : 0.f;
-        a.losses[1] = u ? (float)(bt / (double)u) : 0.f;
+        a.losses[1] = used ? (float)(bt / (double)used) : 0.f;
     }
 }
 
@@ -479,10 +500,8 @@ cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, 
     a.T = c.T; a.chunk = 0; a.E = c.E; a.K = c.K; a.S = (int)S; a.sigmoid = c.score_func == MOE_SCORE_SIGMOID;
     a.c_balance = c_balance; a.c_z = c_z;
     a.w.status = reinterpret_cast<int*>(w + L.head);
-    a.w.bar = reinterpret_cast<int*>(w + L.head + 64);
-    a.w.done = reinterpret_cast<int*>(w + L.head + 80);
-    a.w.used = reinterpret_cast<int*>(w + L.head + 84);
-    a.w.all = reinterpret_cast<unsigned long long*>(w + L.head + 88);
+    a.w.bar = reinterpret_cast<uint32_t*>(w + L.head + 64);
+    a.w.done = reinterpret_cast<uint32_t*>(w + L.head + 128);
     a.w.tokens = reinterpret_cast<int*>(w + L.tokens);
     a.w.bad = reinterpret_cast<int*>(w + L.bad);
     a.w.acc = reinterpret_cast<unsigned long long*>(w + L.acc);
