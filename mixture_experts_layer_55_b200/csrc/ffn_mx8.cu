@@ -89,6 +89,7 @@ struct Misc {
     int row0[MAX_E];
     int rowend[MAX_E];
     int pref[MAX_E + 1];
+    int warp_sum[NUM_THREADS / 32];
 };
 
 template <bool PAIR> constexpr size_t smem_bytes()
@@ -305,27 +306,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tmem_relinquish();
         }
     }
-    // tile table from the offsets (a malformed block is treated as empty)
-    for (int e = threadIdx.x; e < E; e += NUM_THREADS) {
-        m->row0[e] = a.offsets[e];
-        m->rowend[e] = a.offsets[e + 1];
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int run = 0, prev = 0;
-        for (int e = 0; e < E; ++e) {
-            int r0 = m->row0[e], r1 = m->rowend[e];
-            if (r0 < prev || r1 < r0 || (int64_t)r1 > a.max_rows) {
-                raise_flag(a.status, kFlagBounds, 720);
-                r0 = r1 = prev;
-            }
+    // tile table from the offsets, a thread per expert (with offsets that are
+    // malformed anywhere nothing is computed)
+    {
+        const int e = threadIdx.x;
+        int tiles = 0;
+        bool bad = false;
+        if (e < E) {
+            const int r0 = a.offsets[e], r1 = a.offsets[e + 1];
+            bad = r0 < 0 || r1 < r0 || (int64_t)r1 > a.max_rows;
             m->row0[e] = r0;
             m->rowend[e] = r1;
-            prev = r1;
-            m->pref[e] = run;
-            run += (r1 - r0 + BM - 1) / BM * a.n_tiles;
+            if (!bad) tiles = (r1 - r0 + BM - 1) / BM * a.n_tiles;
         }
-        m->pref[E] = run;
+        const bool any_bad = __syncthreads_or(bad) != 0;
+        if (any_bad && threadIdx.x == 0) raise_flag(a.status, kFlagBounds, 720);
+        if (any_bad) tiles = 0;
+        int run = tiles;  // inclusive sum within the warp, then over the warps
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
+        }
+        if (lane == 31) m->warp_sum[warp] = run;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) run += m->warp_sum[w];
+        if (e < E) m->pref[e + 1] = run;
+        if (e == 0) m->pref[0] = 0;
     }
     tc_fence_before();
     if (PAIR) cluster_sync();  // the peer's barriers are initialised before any remote signal
@@ -336,9 +343,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int num_kb = (a.Kdim + BK - 1) / BK;
     volatile int* abort_flag = &m->abort_flag;
 
+    // The down product is launched while the gate/up product still runs: what reads
+    // h waits until that has ended, the rest of its start does not.
+    if (GATEUP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ TMA producer (each CTA)
+            if (!GATEUP) asm volatile("griddepcontrol.wait;" ::: "memory");
             int stage = 0;
             uint32_t phase = 0;
             int last_phase[STAGES];
@@ -499,6 +511,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     } else if (warp < EPI_WARP0) {
         // ------------------------------------------------ scales (each CTA: its A rows, all of B's)
+        if (!GATEUP) asm volatile("griddepcontrol.wait;" ::: "memory");
         const int i = (warp - 2) * 32 + lane;
         const int nb = a.Kdim / kMxBlock, groups = (num_kb + 3) / 4;
         const uint32_t off = (uint32_t)((i & 31) * 16 + (i >> 5) * 4);
@@ -758,24 +771,28 @@ static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, con
     if (e != cudaSuccess) return e;
     int64_t n = tiles_bound < units ? tiles_bound : units;
     if (n < 1) n = 1;
-    constexpr size_t smem = smem_bytes<PAIR>();
-    if (!PAIR) {
-        ffn_mx8_kernel<GATEUP, false><<<(unsigned)n, NUM_THREADS, smem, s>>>(mA, mB0, mB1, a);
-        return cudaGetLastError();
-    }
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(2 * n), 1, 1);
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (PAIR) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = 2;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    if (!GATEUP) {  // may start before the gate/up product has ended
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    cfg.gridDim = dim3((unsigned)(Geo<PAIR>::CTAS * n), 1, 1);
     cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem_bytes<PAIR>();
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, true>, mA, mB0, mB1, a);
+    cfg.numAttrs = na;
+    return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, PAIR>, mA, mB0, mB1, a);
 }
 
 }  // namespace mx
