@@ -28,15 +28,14 @@
 // 480).  The epilogue empties the shared columns first and says so; the next
 // tile's MMAs start then, not when the whole accumulator has been read.
 //
-// Bound: the tensor cores (few, long experts), the stream of weights (decode).
-// Measured on the way (T = 4096, D = F = 4096, 8 experts, K = 2; gate/up and
-// down in us): 461 + 232 with a release at cluster scope for every stage's
-// scales; 351 + 182 with one for every four stages, issued by an idle thread;
-// 276 + 141 with the issuing warp's operands in uniform registers; 232 + 126
-// with scales four groups deep and 32-byte stores.  The MMAs alone take
-// 184 + 97, the loads alone 165 + 84.  T = 8192, D = 4096, F = 14336: 1.49 + 0.76
-// ms, 2570 TFLOP/s.  256 experts, D = 7168, F = 2048, 128 tokens:
-// 1.16 + 0.60 ms, 6.6 TB/s.
+// Bound: the tensor cores, under the power cap.  Measured on the way (T = 4096,
+// D = F = 4096, 8 experts, K = 2; gate/up and down in us): 461 + 232 with a
+// release at cluster scope for every stage's scales; 351 + 182 with one for every
+// four stages, issued by an idle thread; 276 + 141 with the issuing warp's
+// operands in uniform registers; 232 + 126 with scales four groups deep and
+// 32-byte stores.  The MMAs alone take 184 + 97, the loads alone 165 + 84.
+// T = 8192, D = 4096, F = 14336: 2.25 ms for single calls (2570 TFLOP/s), 2.6-2.7 ms
+// back to back at the 1000 W cap (1.33 GHz).
 #include <cuda.h>
 
 #include "internal.h"
@@ -65,6 +64,11 @@ constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 2 + SF_WARPS;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int MAX_E = 256;
+// Average rows per expert up to which tokens are the MMA's columns.  Measured
+// (8 experts, D = 4096, F = 14336; as columns and as rows): 16 rows 227 and 244 us,
+// 32 rows 271 and 244; 64 experts, D = 2048, F = 1408: 6 rows 97 and 100, 24 rows
+// 101 and 105, 32 rows 105 and 104, 48 rows 121 and 106.
+constexpr int kFewRows = 24;
 
 template <bool PAIR> struct Geo {
     static constexpr int CTAS = PAIR ? 2 : 1;
@@ -218,6 +222,36 @@ MOE_DEVICE void decode_tile(const Misc* m, int E, int bm, int bn, int t, int& e,
     n0 = n * bn;
 }
 
+// The tile table from the offsets, a thread per expert (with offsets that are
+// malformed anywhere nothing is computed).  Every thread of the block calls it.
+MOE_DEVICE void build_tiles(Misc* m, const Args& a, int bm)
+{
+    const int e = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int tiles = 0;
+    bool bad = false;
+    if (e < a.E) {
+        const int r0 = a.offsets[e], r1 = a.offsets[e + 1];
+        bad = r0 < 0 || r1 < r0 || (int64_t)r1 > a.max_rows;
+        m->row0[e] = r0;
+        m->rowend[e] = r1;
+        if (!bad) tiles = (r1 - r0 + bm - 1) / bm * a.n_tiles;
+    }
+    const bool any_bad = __syncthreads_or(bad) != 0;
+    if (any_bad && threadIdx.x == 0) raise_flag(a.status, kFlagBounds, 720);
+    if (any_bad) tiles = 0;
+    int run = tiles;  // inclusive sum within the warp, then over the warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+    }
+    if (lane == 31) m->warp_sum[warp] = run;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) run += m->warp_sum[w];
+    if (e < a.E) m->pref[e + 1] = run;
+    if (e == 0) m->pref[0] = 0;
+}
+
 // Scales of stages 4g .. 4g+3 of one row (null: zeros), nb = bytes per row.
 // Rows are 16-byte, 4-byte or only byte aligned with nb.
 MOE_DEVICE uint4 load_scales(const uint8_t* row, int g, int nb)
@@ -306,34 +340,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tmem_relinquish();
         }
     }
-    // tile table from the offsets, a thread per expert (with offsets that are
-    // malformed anywhere nothing is computed)
-    {
-        const int e = threadIdx.x;
-        int tiles = 0;
-        bool bad = false;
-        if (e < E) {
-            const int r0 = a.offsets[e], r1 = a.offsets[e + 1];
-            bad = r0 < 0 || r1 < r0 || (int64_t)r1 > a.max_rows;
-            m->row0[e] = r0;
-            m->rowend[e] = r1;
-            if (!bad) tiles = (r1 - r0 + BM - 1) / BM * a.n_tiles;
-        }
-        const bool any_bad = __syncthreads_or(bad) != 0;
-        if (any_bad && threadIdx.x == 0) raise_flag(a.status, kFlagBounds, 720);
-        if (any_bad) tiles = 0;
-        int run = tiles;  // inclusive sum within the warp, then over the warps
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += v;
-        }
-        if (lane == 31) m->warp_sum[warp] = run;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) run += m->warp_sum[w];
-        if (e < E) m->pref[e + 1] = run;
-        if (e == 0) m->pref[0] = 0;
-    }
+    build_tiles(m, a, BM);
     tc_fence_before();
     if (PAIR) cluster_sync();  // the peer's barriers are initialised before any remote signal
     else __syncthreads();
@@ -685,6 +692,357 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
 }
 
+// ---------------------------------------------------- few rows per expert --
+// The same products with the operands' places exchanged: 128 rows of a weight are
+// the MMA's rows and up to NT tokens its columns, so a tile of few tokens costs NT
+// columns of multiplications instead of 128 padded rows.  (The weight stream is
+// the bound either way, but the padded form draws the card's whole power, and at
+// 880 MHz falls behind the stream: 128 tokens on 256 experts, D = 7168, F = 2048,
+// 1.95 ms, against 1.68 here, 6.9 TB/s.)  A tile is two
+// blocks of 128 weight rows, gate and up of the same 128 of F, or 256 of D, each
+// with an accumulator of NT columns; accumulators and scales are double-buffered in
+// tensor memory side by side.  In the epilogue a lane is a weight row: 32 lanes
+// hold one token's block of 32 along F, whose maximum is one warp reduction.
+template <int NT> struct Few {
+    static constexpr int W_BYTES = 128 * BK;
+    static constexpr int T_BYTES = NT * BK;
+    static constexpr int OP_BYTES = 2 * W_BYTES + T_BYTES;
+    static constexpr int STAGES = 5;
+    static constexpr int SF_COL = 4 * NT;  // behind 2 x 2 accumulators; then A0, A1, B: 4 columns each
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * OP_BYTES + SF_SLOTS * SF_SLOT_BYTES + sizeof(Misc);
+    static constexpr int TMEM = NT == 32 ? 256 : 128;
+    static_assert(SF_COL + 2 * SF_BUF_COLS <= TMEM, "tensor memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <int N> MOE_DEVICE void tmem_ld(uint32_t taddr, uint32_t (&r)[N]);
+template <> MOE_DEVICE void tmem_ld<32>(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
+template <> MOE_DEVICE void tmem_ld<16>(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+template <> MOE_DEVICE void tmem_ld<8>(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+template <bool GATEUP, int NT>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    ffn_mx8_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
+                       const __grid_constant__ CUtensorMap tmW1, const Args a)
+{
+    using G = Few<NT>;
+    constexpr int BN = GATEUP ? 128 : 256, STAGES = G::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* scales = stages + (size_t)STAGES * G::OP_BYTES;
+    Misc* m = reinterpret_cast<Misc*>(scales + (size_t)SF_SLOTS * SF_SLOT_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = a.E, unit = (int)blockIdx.x, units = (int)gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&m->full[s], 1);
+            mbar_init(&m->empty[s], 1);
+        }
+        for (int s = 0; s < SF_SLOTS; ++s) {
+            mbar_init(&m->sfull[s], SF_WARPS);
+            mbar_init(&m->sempty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&m->tfull[b], 1);
+            mbar_init(&m->tempty[b], EPI_WARPS);
+        }
+        mbar_init(&m->drain, 1);
+        m->abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmX);
+        prefetch_tmap(&tmW0);
+        if (GATEUP) prefetch_tmap(&tmW1);
+    }
+    if (warp == 1) {
+        tmem_alloc(&m->tmem_base, G::TMEM);
+        tmem_relinquish();
+    }
+    build_tiles(m, a, NT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = m->tmem_base;
+    const int total = m->pref[E];
+    const int num_kb = (a.Kdim + BK - 1) / BK;
+    volatile int* abort_flag = &m->abort_flag;
+    // the down product starts under the gate/up product's end, as above
+    if (GATEUP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            auto weights = [&](int stage, int kb, int e, int n0) {
+                uint8_t* sW = stages + (size_t)stage * G::OP_BYTES;
+                mbar_arrive_expect_tx(&m->full[stage], G::OP_BYTES);
+                tma_load_3d(sW, &tmW0, kb * BK, n0, e, &m->full[stage]);
+                tma_load_3d(sW + G::W_BYTES, GATEUP ? &tmW1 : &tmW0, kb * BK, GATEUP ? n0 : n0 + 128, e,
+                            &m->full[stage]);
+            };
+            auto tokens = [&](int stage, int kb, int m_row0) {
+                tma_load_2d(stages + (size_t)stage * G::OP_BYTES + 2 * G::W_BYTES, &tmX, kb * BK, m_row0,
+                            &m->full[stage]);
+            };
+            int stage = 0;
+            uint32_t phase = 0;
+            int last_phase[STAGES];
+            for (int s = 0; s < STAGES; ++s) last_phase[s] = -1;
+            bool ok = true;
+            // down: the first stages' weights do not wait for h
+            int early = 0;
+            if (!GATEUP) {
+                if (unit < total) {
+                    int e, m_row0, row_end, n0;
+                    decode_tile(m, E, NT, BN, unit, e, m_row0, row_end, n0);
+                    early = num_kb < STAGES ? num_kb : STAGES;
+                    for (int kb = 0; kb < early; ++kb) weights(kb, kb, e, n0);
+                }
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+            }
+            for (int t = unit; t < total && ok; t += units) {
+                int e, m_row0, row_end, n0;
+                decode_tile(m, E, NT, BN, t, e, m_row0, row_end, n0);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait(&m->empty[stage], phase ^ 1u, a.status, 742, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (early > 0) --early;
+                    else weights(stage, kb, e, n0);
+                    tokens(stage, kb, m_row0);
+                    last_phase[stage] = (int)phase;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // never leave the CTA with a copy in flight (after an abort: stages whose
+            // weights came early get their tokens too, so that their phase completes)
+            for (int s = 0; early > 0 && s < STAGES; ++s)
+                if (last_phase[s] < 0) {
+                    tokens(s, 0, 0);
+                    last_phase[s] = 0;
+                    --early;
+                }
+            for (int s = 0; s < STAGES; ++s)
+                if (last_phase[s] >= 0) mbar_wait(&m->full[s], (uint32_t)last_phase[s], a.status, 743, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc = mx_idesc(128, NT);
+        const uint32_t leader = elect_one();
+        const uint32_t tbase = __shfl_sync(0xffffffffu, tmem_base, 0);
+        const int tiles = __shfl_sync(0xffffffffu, total, 0);
+        const uint32_t s_stages = __shfl_sync(0xffffffffu, smem_u32(stages), 0);
+        const uint32_t s_scales = __shfl_sync(0xffffffffu, smem_u32(scales), 0);
+        const uint32_t s_empty = __shfl_sync(0xffffffffu, smem_u32(&m->empty[0]), 0);
+        const uint32_t s_sempty = __shfl_sync(0xffffffffu, smem_u32(&m->sempty[0]), 0);
+        const uint32_t s_tfull = __shfl_sync(0xffffffffu, smem_u32(&m->tfull[0]), 0);
+        int stage = 0, acc = 0, slot = 0, in_slot = 0;
+        uint32_t phase = 0, acc_phase = 0, sphase = 0;
+        bool ok = true;
+        for (int t = unit; t < tiles && ok; t += units) {
+            if (!warp_wait_all(&m->tempty[acc], acc_phase ^ 1u, a.status, 744, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t d0 = tbase + (uint32_t)(acc * 2 * NT);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if ((in_slot == 0 && !warp_wait_all(&m->sfull[slot], sphase, a.status, 747, abort_flag)) ||
+                    !warp_wait_all(&m->full[stage], phase, a.status, 746, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tsf = tbase + G::SF_COL + (uint32_t)((kb & 1) * SF_BUF_COLS);
+                const uint64_t sdesc = scale_desc(s_scales + (uint32_t)(slot * SF_SLOT_BYTES + in_slot * SF_BYTES));
+                copy_scales<false>(leader, tsf, sdesc);                     // the tokens'
+                copy_scales<false>(leader, tsf + 4, sdesc + (512 >> 4));    // the weights'
+                copy_scales<false>(leader, tsf + 8, sdesc + (1024 >> 4));
+                const uint64_t wdesc = umma_desc_sw128(s_stages + (uint32_t)stage * G::OP_BYTES, 16, 1024);
+                const uint64_t xdesc = wdesc + (2 * G::W_BYTES >> 4);
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        mma_mx8<false>(leader, d0 + b * NT, wdesc + (b * G::W_BYTES >> 4) + kk * 2, xdesc + kk * 2,
+                                       idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), tsf + 4 + 4 * b, tsf,
+                                       kk != 0 ? 1u : (kb != 0 ? 1u : 0u));
+                commit<false>(leader, s_empty + (uint32_t)stage * 8);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++in_slot == SF_GROUP || kb == num_kb - 1) {
+                    commit<false>(leader, s_sempty + (uint32_t)slot * 8);
+                    in_slot = 0;
+                    if (++slot == SF_SLOTS) {
+                        slot = 0;
+                        sphase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) break;
+            commit<false>(leader, s_tfull + (uint32_t)acc * 8);
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        __syncwarp();
+        if (leader) umma_commit(&m->drain);
+        __syncwarp();
+        warp_wait_all(&m->drain, 0, a.status, 748, nullptr);
+    } else if (warp < EPI_WARP0) {
+        // ------------------------------------------------ scales
+        const int i = (warp - 2) * 32 + lane;
+        const int nb = a.Kdim / kMxBlock, groups = (num_kb + 3) / 4;
+        const uint32_t off = (uint32_t)((i & 31) * 16 + (i >> 5) * 4);
+        const uint8_t *px = nullptr, *pw0 = nullptr, *pw1 = nullptr;
+        auto rows_of = [&](int t) {
+            int e, m_row0, row_end, n0;
+            decode_tile(m, E, NT, BN, t, e, m_row0, row_end, n0);
+            const int64_t row = (int64_t)m_row0 + i;
+            px = i < NT && row < row_end ? a.as + row * nb : nullptr;
+            const int n = n0 + i, n2 = GATEUP ? n : n + 128;
+            const int64_t be = (int64_t)e * a.N;
+            pw0 = n < a.N ? a.b0s + (be + n) * nb : nullptr;
+            pw1 = n2 < a.N ? (GATEUP ? a.b1s : a.b0s) + (be + n2) * nb : nullptr;
+        };
+        uint4 vx[2], v0[2], v1[2];
+        int ld_t = unit, ld_g = 0;
+        auto load_weights = [&](int i2) {
+            v0[i2] = load_scales(pw0, ld_g, nb);
+            v1[i2] = load_scales(pw1, ld_g, nb);
+        };
+        auto load_tokens = [&](int i2) { vx[i2] = load_scales(px, ld_g, nb); };
+        auto load_next = [&](int i2) {
+            if (ld_t >= total) return;
+            if (ld_g == 0) rows_of(ld_t);
+            load_weights(i2);
+            load_tokens(i2);
+            if (++ld_g == groups) {
+                ld_g = 0;
+                ld_t += units;
+            }
+        };
+        if (!GATEUP) asm volatile("griddepcontrol.wait;" ::: "memory");
+        load_next(0);
+        load_next(1);
+        int slot = 0, kb_left = num_kb;
+        uint32_t sphase = 0;
+        const int64_t mine = unit < total ? (int64_t)((total - unit + units - 1) / units) * groups : 0;
+        for (int64_t n = 0; n < mine; n += 2) {
+            bool ok = true;
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+                if (n + i2 >= mine) break;
+                if (!warp_wait(&m->sempty[slot], sphase ^ 1u, lane, a.status, 749, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* dst = scales + (size_t)slot * SF_SLOT_BYTES + off;
+#pragma unroll
+                for (int k = 0; k < SF_GROUP; ++k) {
+                    *reinterpret_cast<uint32_t*>(dst + k * SF_BYTES) = word_of(vx[i2], k);
+                    *reinterpret_cast<uint32_t*>(dst + k * SF_BYTES + 512) = word_of(v0[i2], k);
+                    *reinterpret_cast<uint32_t*>(dst + k * SF_BYTES + 1024) = word_of(v1[i2], k);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m->sfull[slot]);
+                if (++slot == SF_SLOTS) {
+                    slot = 0;
+                    sphase ^= 1u;
+                }
+                kb_left -= SF_GROUP;
+                if (kb_left <= 0) kb_left = num_kb;
+                load_next(i2);
+            }
+            if (!ok) break;
+        }
+    } else {
+        // ------------------------------------------------ epilogue: lane = weight row
+        const int quad = warp & 3;
+        const int half = (warp - EPI_WARP0) >> 2;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int t = unit; t < total; t += units) {
+            int e, m_row0, row_end, n0;
+            decode_tile(m, E, NT, BN, t, e, m_row0, row_end, n0);
+            const int rows = row_end - m_row0 < NT ? row_end - m_row0 : NT;
+            float w = 1.f;  // lane j: token j's weight
+            if (!GATEUP && a.perm != nullptr && lane < rows) {
+                const int32_t pa = a.perm[m_row0 + lane];
+                w = 0.f;
+                if (pa >= 0 && (int64_t)pa < a.nk) w = a.topk_w[pa];
+                else if (half == 0) raise_flag(a.status, kFlagBounds, 741);
+            }
+            if (!warp_wait(&m->tfull[acc], acc_phase, lane, a.status, 750, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * 2 * NT);
+            if (GATEUP) {  // this half's tokens
+                constexpr int H = NT / 2;
+                uint32_t g[H], u[H];
+                tmem_ld<H>(taddr + half * H, g);
+                tmem_ld<H>(taddr + NT + half * H, u);
+                tmem_ld_wait();
+                const int f0 = n0 + quad * 32;
+                if (f0 < a.N) {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) {
+                        const int r = half * H + j;
+                        if (r >= rows) break;
+                        const float h = swiglu(__uint_as_float(g[j]), __uint_as_float(u[j]));
+                        const uint32_t b = mx_scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(h)));
+                        const int64_t row = (int64_t)m_row0 + r;
+                        a.h[row * a.N + f0 + lane] = (uint8_t)mx_pack4(h, 0.f, 0.f, 0.f, mx_inv_scale(b));
+                        if (lane == 0) a.hs[row * (a.N / kMxBlock) + f0 / kMxBlock] = (uint8_t)b;
+                    }
+                }
+            } else {  // this half's 128 rows of D
+                uint32_t v[NT];
+                tmem_ld<NT>(taddr + half * NT, v);
+                tmem_ld_wait();
+                const int d0 = n0 + half * 128 + quad * 32;
+                if (d0 < a.N) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        if (j >= rows) break;
+                        const float wj = __shfl_sync(0xffffffffu, w, j);
+                        a.y[((int64_t)m_row0 + j) * a.N + d0 + lane] = __float2bfloat16_rn(wj * __uint_as_float(v[j]));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->tempty[acc]);
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, G::TMEM);
+    }
+}
+
 // ------------------------------------------------------------------- host --
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -795,6 +1153,29 @@ static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, con
     return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, PAIR>, mA, mB0, mB1, a);
 }
 
+template <bool GATEUP, int NT>
+static cudaError_t launch_few(const CUtensorMap& mX, const CUtensorMap& mW0, const CUtensorMap& mW1, const Args& a,
+                              int64_t tiles_bound, cudaStream_t s)
+{
+    static PerDeviceFlag opted;
+    int dev = 0, sms = 0;
+    cudaError_t e = opt_in_smem(opted, reinterpret_cast<const void*>(ffn_mx8_few_kernel<GATEUP, NT>), Few<NT>::SMEM);
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(tiles_bound < sms ? tiles_bound : sms), 1, 1);
+    cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Few<NT>::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = GATEUP ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, ffn_mx8_few_kernel<GATEUP, NT>, mX, mW0, mW1, a);
+}
+
 }  // namespace mx
 
 cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq, const void* xs,
@@ -805,7 +1186,27 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
     using namespace mx;
     auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
     const uint64_t D = (uint64_t)c.D, F = (uint64_t)c.F, E = (uint64_t)c.E, R = (uint64_t)max_rows;
+    Args a{};
+    a.offsets = offsets; a.perm = perm; a.topk_w = topk_w;
+    a.as = u8(xs); a.b0s = u8(w.gate_scales); a.b1s = u8(w.up_scales);
+    a.h = static_cast<uint8_t*>(hq); a.hs = static_cast<uint8_t*>(hs);
+    a.E = c.E; a.Kdim = c.D; a.N = c.F; a.n_tiles = (c.F + 127) / 128;
+    a.max_rows = max_rows; a.nk = c.T * c.K; a.status = status;
+    Args d = a;  // the down product
+    d.as = u8(hs); d.b0s = d.b1s = u8(w.down_scales);
+    d.y = static_cast<__nv_bfloat16*>(y_perm);
+    d.Kdim = c.F; d.N = c.D; d.n_tiles = (c.D + 255) / 256;
     CUtensorMap mX, mG, mU, mH, mD;
+    if (max_rows <= kFewRows * (int64_t)c.E) {
+        constexpr int NT = 32;
+        if (!map_bytes(&mX, xq, D, R, 0, NT) || !map_bytes(&mG, w.gate, D, F, E, 128) ||
+            !map_bytes(&mU, w.up, D, F, E, 128) || !map_bytes(&mH, hq, F, R, 0, NT) ||
+            !map_bytes(&mD, w.down, F, D, E, 128))
+            return cudaErrorInvalidValue;
+        const int64_t mt = max_rows < c.E ? max_rows : (max_rows + NT - 1) / NT + c.E;
+        cudaError_t e = launch_few<true, NT>(mX, mG, mU, a, mt * a.n_tiles, s);
+        return e != cudaSuccess ? e : launch_few<false, NT>(mH, mD, mD, d, mt * d.n_tiles, s);
+    }
     if (!map_bytes(&mX, xq, D, R, 0, 128) || !map_bytes(&mG, w.gate, D, F, E, 64) ||
         !map_bytes(&mU, w.up, D, F, E, 64) || !map_bytes(&mH, hq, F, R, 0, 128) ||
         !map_bytes(&mD, w.down, F, D, E, 64))
@@ -823,21 +1224,13 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
         if (e != cudaSuccess) return e;
         gm = static_cast<const CUtensorMap*>(amaps);
     }
-    Args a{};
-    a.offsets = offsets; a.perm = perm; a.topk_w = topk_w;
-    a.as = u8(xs); a.b0s = u8(w.gate_scales); a.b1s = u8(w.up_scales);
-    a.h = static_cast<uint8_t*>(hq); a.hs = static_cast<uint8_t*>(hs);
-    a.E = c.E; a.Kdim = c.D; a.N = c.F; a.n_tiles = (c.F + 127) / 128;
-    a.max_rows = max_rows; a.nk = c.T * c.K; a.status = status; a.amaps = gm;
+    a.amaps = gm;
+    d.amaps = gm ? gm + c.E : nullptr;
     cudaError_t e = pair ? launch_one<true, true>(mX, mG, mU, a, mt * a.n_tiles, s)
                          : launch_one<true, false>(mX, mG, mU, a, mt * a.n_tiles, s);
     if (e != cudaSuccess) return e;
-    a.as = u8(hs); a.b0s = a.b1s = u8(w.down_scales);
-    a.y = static_cast<__nv_bfloat16*>(y_perm);
-    a.Kdim = c.F; a.N = c.D; a.n_tiles = (c.D + 255) / 256;
-    a.amaps = gm ? gm + c.E : nullptr;
-    return pair ? launch_one<false, true>(mH, mD, mD, a, mt * a.n_tiles, s)
-                : launch_one<false, false>(mH, mD, mD, a, mt * a.n_tiles, s);
+    return pair ? launch_one<false, true>(mH, mD, mD, d, mt * d.n_tiles, s)
+                : launch_one<false, false>(mH, mD, mD, d, mt * d.n_tiles, s);
 }
 
 }  // namespace moe

@@ -439,7 +439,8 @@ def _check_experts(st, hq, hs, y, weighted=True):
 EXPERTS = [(1, 32, 32, 1, 1, None), (1, 256, 512, 8, 2, None), (3, 96, 160, 2, 2, None), (5, 64, 32, 4, 1, [0, 5, 0, 0]),
            (40, 224, 288, 3, 2, [79, 0, 1]), (129, 256, 96, 1, 1, None), (300, 128, 64, 5, 2, [128, 129, 0, 127, 216]),
            (64, 512, 1408, 64, 6, None), (1000, 160, 416, 4, 2, [256, 257, 1, 1486]), (700, 1024, 544, 2, 1, [333, 367]),
-           (4, 7168, 64, 256, 8, None), (2000, 2048, 256, 8, 2, None)]
+           (4, 7168, 64, 256, 8, None), (2000, 2048, 256, 8, 2, None), (60, 224, 160, 8, 2, [70, 0, 33, 1, 16, 0, 0, 0]),
+           (20, 1408, 2080, 4, 2, None), (96, 32, 544, 8, 2, [0, 32, 32, 64, 31, 33, 0, 0])]
 
 
 @pytest.mark.parametrize("case", range(len(EXPERTS)))
