@@ -86,11 +86,25 @@ MOE_DEVICE float row_add(float v, float* red, int warps)
     return t;
 }
 
+// The same with the warps' sums (a thread's at most 64 squares and five additions
+// in fp32) added in fp64.
+MOE_DEVICE double row_add_wide(float v, float* red, int warps)
+{
+    v = warp_add(v);
+    if (warps == 1) return (double)v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double t = 0.0;
+    for (int w = 0; w < warps; ++w) t += (double)red[w];
+    return t;
+}
+
 struct NormArgs {
     int64_t T;
     int D, nvec;     // nvec = D / 8
     int warps;       // warps per row
     float eps;
+    double inv_d;    // 1 / D
     const float* gamma;
     float* rstd;     // (T) or null
     uint8_t* q;      // (T, D) or null
@@ -123,7 +137,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
             }
         }
     };
-    constexpr bool AHEAD = VPT * MAXT <= 1024;  // wider rows need the registers
+    constexpr bool AHEAD = VPT * MAXT * (int)sizeof(T) <= 4096;  // else the registers are needed
     if (AHEAD && team < a.T) fetch(team);
     int flip = 0;
     for (int64_t row = team; row < a.T; row += step, flip ^= 1) {
@@ -148,8 +162,14 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
             }
         }
         if (AHEAD && row + step < a.T) fetch(row + step);
-        ss = row_add(ss, red[flip], a.warps);
-        const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+        // rstd as the sum of two fp32 values, from fp32's root and one Newton step in
+        // fp64: n is then the formula's to 2^-24, and what is rounded further, to bf16
+        // and to 8 bits, falls on the formula's side of a border
+        const double mean = row_add_wide(ss, red[flip], a.warps) * a.inv_d + (double)a.eps;
+        const float r0 = rsqrtf((float)mean);
+        const double r2 = (double)r0 * (1.5 - 0.5 * mean * (double)r0 * (double)r0);
+        const bool plain = r0 > 0.f && r0 < INFINITY;  // else r0 says it: zeros without eps, overflow, NaN
+        const float r = plain ? (float)r2 : r0, r_lo = plain ? (float)(r2 - (double)r) : 0.f;
         if (tid == 0 && a.rstd != nullptr) a.rstd[row] = r;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -159,7 +179,12 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
                 float g[8];
                 load_row8<float>(a.gamma + 8 * c, g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
+                for (int j = 0; j < 8; ++j) {  // v r g with its roundings' errors carried along
+                    const float t = v[i][j] * r, n = t * g[j];
+                    const float et = fmaf(v[i][j], r_lo, fmaf(v[i][j], r, -t));
+                    const float en = fmaf(et, g[j], fmaf(t, g[j], -n));
+                    v[i][j] = isfinite(en) ? n + en : n;
+                }
                 R::store(n_out != nullptr ? n_out + base + 8 * c : nullptr, v[i]);
             }
             if (a.q != nullptr) {
@@ -187,21 +212,30 @@ struct NormBwdArgs {
     int D, nvec, warps;
     const float* gamma;
     const float* rstd;
-    float* part;  // (gridDim.x * rows per block, D): each row team's share of dgamma
+    float* part;  // (gridDim.x, D): each block's share of dgamma
 };
 
-// A team of `warps` warps walks rows; each thread keeps its columns' share of
-// dgamma in registers and writes it once, so dn and s cross memory once.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_backward_kernel(const T* dn, const T* ds, const T* s, T* dx, const NormBwdArgs a)
+// A team of `warps` warps (a block, or with warps = 1 each of its warps) walks
+// rows; each thread keeps its columns' share of dgamma in registers and the block
+// writes its share once, so dn and s cross memory once.  Where a thread has more
+// than one vector the row is held as it was loaded and widened twice, before and
+// after its sum (held in fp32, D = 12288 took 211 us for 2048 rows, spilled; 57 so);
+// the next row is on its way meanwhile.  T = 8192, D = 4096
+// bf16: 48.9 us with dgamma, 0.84 of the measured copy bandwidth.
+template <typename T, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const T* dn, const T* ds, const T* s, T* dx,
+                                                                const NormBwdArgs a)
 {
     __shared__ float red[2][32];
+    extern __shared__ float share[];  // (warps of the block, D) where each warp has rows of its own
+    using R = Row8<T>;
     const int tpr = a.warps * 32;
     const int teams = a.warps == 1 ? (int)(blockDim.x >> 5) : 1;
     const int64_t team = a.warps == 1 ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = (int64_t)gridDim.x * teams;
     const int tid = a.warps == 1 ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-    using R = Row8<T>;
+    constexpr bool AHEAD = VPT * MAXT * (int)sizeof(T) <= 2048;  // else the registers are needed
+    constexpr bool KEEP = VPT == 1 && sizeof(T) == 2;  // the widened row fits the registers
     float acc[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -209,7 +243,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_backward_kernel(const
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     typename R::Raw rs[VPT], rn[VPT], rd[VPT];
     float r_next = 0.f;
-    auto fetch = [&](int64_t row) {  // the next row, while one is reduced and written
+    auto fetch = [&](int64_t row) {
         r_next = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -221,31 +255,36 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_backward_kernel(const
             }
         }
     };
-    constexpr bool AHEAD = VPT == 1;  // wider rows need the registers
     if (AHEAD && team < a.T) fetch(team);
     int flip = 0;
     for (int64_t row = team; row < a.T; row += step, flip ^= 1) {
         const int64_t base = row * a.D;
         if (!AHEAD) fetch(row);
         const float r = r_next;
-        float xh[VPT][8], g[VPT][8];
-        typename R::Raw d0[VPT];
+        typename R::Raw cs[VPT], cn[VPT], cd[VPT];
+        float xk[KEEP ? VPT : 1][8], gk[KEEP ? VPT : 1][8];
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = tid + i * tpr;
+            cs[i] = rs[i];
+            cn[i] = rn[i];
+            cd[i] = rd[i];
             if (c < a.nvec) {
-                float w[8];
-                R::values(rs[i], xh[i]);
-                R::values(rn[i], g[i]);
-                d0[i] = rd[i];
+                float xh[8], g[8], w[8];
+                R::values(cs[i], xh);
+                R::values(cn[i], g);
                 load_row8<float>(a.gamma + 8 * c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    xh[i][j] *= r;
-                    acc[i][j] = fmaf(g[i][j], xh[i][j], acc[i][j]);
-                    g[i][j] *= w[j];
-                    dot = fmaf(g[i][j], xh[i][j], dot);
+                    xh[j] *= r;
+                    acc[i][j] = fmaf(g[j], xh[j], acc[i][j]);
+                    g[j] *= w[j];
+                    dot = fmaf(g[j], xh[j], dot);
+                    if (KEEP) {
+                        xk[KEEP ? i : 0][j] = xh[j];
+                        gk[KEEP ? i : 0][j] = g[j];
+                    }
                 }
             }
         }
@@ -255,26 +294,52 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_backward_kernel(const
         for (int i = 0; i < VPT; ++i) {
             const int c = tid + i * tpr;
             if (c < a.nvec) {
-                float o[8];
-                if (ds != nullptr) R::values(d0[i], o);
+                float xh[8], g[8], w[8], o[8];
+                if (!KEEP) {
+                    R::values(cs[i], xh);
+                    R::values(cn[i], g);
+                    load_row8<float>(a.gamma + 8 * c, w);
+                }
+                if (ds != nullptr) R::values(cd[i], o);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float d = r * (g[i][j] - xh[i][j] * dot);
+                    if (KEEP) {
+                        xh[j] = xk[KEEP ? i : 0][j];
+                        g[j] = gk[KEEP ? i : 0][j];
+                    } else {
+                        xh[j] *= r;
+                        g[j] *= w[j];
+                    }
+                    const float d = r * (g[j] - xh[j] * dot);
                     o[j] = ds != nullptr ? d + o[j] : d;
                 }
                 R::store(dx + base + 8 * c, o);
             }
         }
     }
+    if (a.warps == 1) {  // the block's warps add up first
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = tid + i * tpr;
+            if (c < a.nvec) Row8<float>::store(share + (threadIdx.x >> 5) * a.D + 8 * c, acc[i]);
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
+            float t = 0.f;
+            for (int w = 0; w < teams; ++w) t += share[w * a.D + d];
+            a.part[(int64_t)blockIdx.x * a.D + d] = t;
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = tid + i * tpr;
-        if (c < a.nvec) Row8<float>::store(a.part + team * a.D + 8 * c, acc[i]);
+        if (c < a.nvec) Row8<float>::store(a.part + (int64_t)blockIdx.x * a.D + 8 * c, acc[i]);
     }
 }
 
-// dgamma[d] = sum of the teams' shares: 8 warps per 32 columns, each with every
-// 8th team, then added in order.
+// dgamma[d] = sum of the blocks' shares: 8 warps per 32 columns, each with every
+// 8th block, then added in order.
 __global__ void __launch_bounds__(256) rmsnorm_dgamma_kernel(const float* part, int teams, int D, float* dgamma)
 {
     __shared__ float sum[8][33];
@@ -315,76 +380,134 @@ static NormPlan norm_plan(int D, int most_threads)
     return p;
 }
 
-template <typename T>
-static cudaError_t launch_norm_t(int64_t rows, int D, const void* x, const void* residual, void* s_out,
-                                 void* n_out, const NormArgs& a, const NormPlan& p, cudaStream_t s)
+// One wave: as many row teams as are resident at once (T = 8192, D = 4096: 46.2 us
+// with a third more blocks than that).
+template <typename T, int VPT, int MAXT>
+static cudaError_t launch_norm_v(int64_t rows, const T* x, const T* residual, T* s_out, T* n_out, const NormArgs& a,
+                                 const NormPlan& p, cudaStream_t s)
 {
-    const int64_t need = (rows + p.rows_per_block - 1) / p.rows_per_block;
-    const int64_t most = 148 * (int64_t)(2048 / p.threads);
-    const unsigned grid = (unsigned)(need < most ? need : most);
+    static std::atomic<int> cached[33];  // resident blocks per SM, by warps in a block (0: not yet asked)
+    auto kernel = rmsnorm_kernel<T, VPT, MAXT>;
+    const int w = p.threads / 32;
+    int per_sm = cached[w].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, p.threads, 0);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        cached[w].store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t need = (rows + p.rows_per_block - 1) / p.rows_per_block, most = 148 * (int64_t)per_sm;
+    kernel<<<(unsigned)(need < most ? need : most), p.threads, 0, s>>>(x, residual, s_out, n_out, a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t launch_norm_t(int64_t rows, const void* x, const void* residual, void* s_out, void* n_out,
+                                 const NormArgs& a, const NormPlan& p, cudaStream_t s)
+{
     const T *px = static_cast<const T*>(x), *pr = static_cast<const T*>(residual);
     T *ps = static_cast<T*>(s_out), *pn = static_cast<T*>(n_out);
-    if (p.threads <= 256 && p.vpt == 2) rmsnorm_kernel<T, 2, 256><<<grid, p.threads, 0, s>>>(px, pr, ps, pn, a);
-    else if (p.threads <= 256 && p.vpt == 4) rmsnorm_kernel<T, 4, 256><<<grid, p.threads, 0, s>>>(px, pr, ps, pn, a);
-    else if (p.vpt == 1) rmsnorm_kernel<T, 1, 1024><<<grid, p.threads, 0, s>>>(px, pr, ps, pn, a);
-    else if (p.vpt == 2) rmsnorm_kernel<T, 2, 1024><<<grid, p.threads, 0, s>>>(px, pr, ps, pn, a);
-    else if (p.vpt == 4) rmsnorm_kernel<T, 4, 1024><<<grid, p.threads, 0, s>>>(px, pr, ps, pn, a);
-    else rmsnorm_kernel<T, 8, 1024><<<grid, p.threads, 0, s>>>(px, pr, ps, pn, a);
-    return cudaGetLastError();
+    if (p.vpt == 1) return launch_norm_v<T, 1, 1024>(rows, px, pr, ps, pn, a, p, s);
+    if (p.threads <= 256 && p.vpt == 2) return launch_norm_v<T, 2, 256>(rows, px, pr, ps, pn, a, p, s);
+    if (p.threads <= 256 && p.vpt == 4) return launch_norm_v<T, 4, 256>(rows, px, pr, ps, pn, a, p, s);
+    if (p.threads <= 512 && p.vpt == 4) return launch_norm_v<T, 4, 512>(rows, px, pr, ps, pn, a, p, s);
+    if (p.vpt == 2) return launch_norm_v<T, 2, 1024>(rows, px, pr, ps, pn, a, p, s);
+    if (p.vpt == 4) return launch_norm_v<T, 4, 1024>(rows, px, pr, ps, pn, a, p, s);
+    return launch_norm_v<T, 8, 1024>(rows, px, pr, ps, pn, a, p, s);
 }
 
 cudaError_t launch_rmsnorm(int64_t T, int D, int dtype, const void* x, const void* residual, const float* gamma,
                            float eps, void* s_out, void* n_out, float* rstd, void* q, void* scales,
                            cudaStream_t s)
 {
-    const NormPlan p = norm_plan(D, T >= 4 * 148 && D <= 8192 ? 256 : kNormMaxThreads);
-    const NormArgs a{T, D, D / 8, p.warps, eps, gamma, rstd, static_cast<uint8_t*>(q), static_cast<uint8_t*>(scales)};
-    return dtype == MOE_BF16 ? launch_norm_t<__nv_bfloat16>(T, D, x, residual, s_out, n_out, a, p, s)
-                             : launch_norm_t<float>(T, D, x, residual, s_out, n_out, a, p, s);
+    const NormPlan p = norm_plan(D, T < 4 * 148 ? kNormMaxThreads : D <= 8192 ? 256 : 512);
+    const NormArgs a{T, D, D / 8, p.warps, eps, 1.0 / D, gamma, rstd, static_cast<uint8_t*>(q), static_cast<uint8_t*>(scales)};
+    return dtype == MOE_BF16 ? launch_norm_t<__nv_bfloat16>(T, x, residual, s_out, n_out, a, p, s)
+                             : launch_norm_t<float>(T, x, residual, s_out, n_out, a, p, s);
 }
 
-// Row teams of the backward, a function of the shape alone (the workspace holds
-// one row of dgamma for each).
+// The backward: up to 1024 elements a warp has rows of its own (eight warps a
+// block); wider rows are a block's, 512 threads of up to four vectors, and beyond
+// 16384 elements 1024 threads.
+static NormPlan norm_bwd_plan(int D)
+{
+    if (D > 1024) return norm_plan(D, D <= 16384 ? 512 : kNormMaxThreads);
+    NormPlan p;
+    p.vpt = D <= 256 ? 1 : D <= 512 ? 2 : 4;
+    p.warps = 1;
+    p.threads = 256;
+    p.rows_per_block = 8;
+    return p;
+}
+
+// Its blocks, a function of the shape alone (the workspace holds one row of dgamma
+// for each).
 static int64_t norm_bwd_blocks(int64_t T, const NormPlan& p)
 {
     const int64_t need = (T + p.rows_per_block - 1) / p.rows_per_block;
-    const int64_t most = 148 * 2;
+    const int64_t most = 148 * (p.threads > 512 ? 1 : p.threads > 256 ? 2 : 4);
     return need < most ? need : most;
 }
 
 size_t rmsnorm_backward_bytes(int64_t T, int D)
 {
-    const NormPlan p = norm_plan(D, kNormMaxThreads);
-    return 256 + align_up((size_t)norm_bwd_blocks(T, p) * p.rows_per_block * D * sizeof(float));
+    return 256 + align_up((size_t)norm_bwd_blocks(T, norm_bwd_plan(D)) * D * sizeof(float));
+}
+
+// *blocks: in, the most the workspace holds; out, the blocks launched (one wave).
+template <typename T, int VPT, int MAXT>
+static cudaError_t launch_norm_bwd_v(int64_t* blocks, const T* dn, const T* ds, const T* s_in, T* dx,
+                                     const NormBwdArgs& a, const NormPlan& p, cudaStream_t s)
+{
+    const size_t smem = p.warps == 1 ? (size_t)p.rows_per_block * a.D * sizeof(float) : 0;  // at most 32 KB
+    static std::atomic<int> cached[33];  // resident blocks per SM, by warps in a block (0: not yet asked)
+    auto kernel = rmsnorm_backward_kernel<T, VPT, MAXT>;
+    const int w = p.threads / 32;
+    int per_sm = cached[w].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, p.threads,
+                                                                      p.warps == 1 ? VPT * 256 * 8 * sizeof(float) : 0);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        cached[w].store(per_sm, std::memory_order_relaxed);
+    }
+    if (*blocks > 148 * (int64_t)per_sm) *blocks = 148 * (int64_t)per_sm;
+    kernel<<<(unsigned)*blocks, p.threads, smem, s>>>(dn, ds, s_in, dx, a);
+    return cudaGetLastError();
 }
 
 template <typename T>
-static void launch_norm_bwd_t(unsigned grid, const void* dn, const void* ds, const void* s_in, void* dx,
-                              const NormBwdArgs& a, const NormPlan& p, cudaStream_t s)
+static cudaError_t launch_norm_bwd_t(int64_t* blocks, const void* dn, const void* ds, const void* s_in, void* dx,
+                                     const NormBwdArgs& a, const NormPlan& p, cudaStream_t s)
 {
     const T *pd = static_cast<const T*>(dn), *pe = static_cast<const T*>(ds), *ps = static_cast<const T*>(s_in);
     T* px = static_cast<T*>(dx);
-    switch (p.vpt) {
-    case 1: rmsnorm_backward_kernel<T, 1><<<grid, p.threads, 0, s>>>(pd, pe, ps, px, a); break;
-    case 2: rmsnorm_backward_kernel<T, 2><<<grid, p.threads, 0, s>>>(pd, pe, ps, px, a); break;
-    case 4: rmsnorm_backward_kernel<T, 4><<<grid, p.threads, 0, s>>>(pd, pe, ps, px, a); break;
-    default: rmsnorm_backward_kernel<T, 8><<<grid, p.threads, 0, s>>>(pd, pe, ps, px, a); break;
+    if (p.warps == 1) {
+        if (p.vpt == 1) return launch_norm_bwd_v<T, 1, 256>(blocks, pd, pe, ps, px, a, p, s);
+        if (p.vpt == 2) return launch_norm_bwd_v<T, 2, 256>(blocks, pd, pe, ps, px, a, p, s);
+        return launch_norm_bwd_v<T, 4, 256>(blocks, pd, pe, ps, px, a, p, s);
     }
+    if (p.threads <= 512) {
+        if (p.vpt == 1) return launch_norm_bwd_v<T, 1, 512>(blocks, pd, pe, ps, px, a, p, s);
+        if (p.vpt == 2) return launch_norm_bwd_v<T, 2, 512>(blocks, pd, pe, ps, px, a, p, s);
+        return launch_norm_bwd_v<T, 4, 512>(blocks, pd, pe, ps, px, a, p, s);
+    }
+    if (p.vpt <= 4) return launch_norm_bwd_v<T, 4, 1024>(blocks, pd, pe, ps, px, a, p, s);
+    return launch_norm_bwd_v<T, 8, 1024>(blocks, pd, pe, ps, px, a, p, s);
 }
 
 cudaError_t launch_rmsnorm_backward(int64_t T, int D, int dtype, const void* dn, const void* ds, const void* s_in,
                                     const float* gamma, const float* rstd, void* dx, float* dgamma, void* ws,
                                     cudaStream_t s)
 {
-    const NormPlan p = norm_plan(D, kNormMaxThreads);
-    const int64_t blocks = norm_bwd_blocks(T, p);
+    const NormPlan p = norm_bwd_plan(D);
+    int64_t blocks = norm_bwd_blocks(T, p);
     float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
     const NormBwdArgs a{T, D, D / 8, p.warps, gamma, rstd, part};
-    if (dtype == MOE_BF16) launch_norm_bwd_t<__nv_bfloat16>((unsigned)blocks, dn, ds, s_in, dx, a, p, s);
-    else launch_norm_bwd_t<float>((unsigned)blocks, dn, ds, s_in, dx, a, p, s);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = dtype == MOE_BF16 ? launch_norm_bwd_t<__nv_bfloat16>(&blocks, dn, ds, s_in, dx, a, p, s)
+                                      : launch_norm_bwd_t<float>(&blocks, dn, ds, s_in, dx, a, p, s);
     if (e != cudaSuccess) return e;
-    rmsnorm_dgamma_kernel<<<(D + 31) / 32, 256, 0, s>>>(part, (int)(blocks * p.rows_per_block), D, dgamma);
+    rmsnorm_dgamma_kernel<<<(D + 31) / 32, 256, 0, s>>>(part, (int)blocks, D, dgamma);
     return cudaGetLastError();
 }
 
