@@ -25,15 +25,18 @@
 // memory; its first tokens' softmax), and then waits.  A block takes consecutive
 // tokens, a token a group of L lanes with 8 experts each, so that a warp is full
 // for 8 experts as for 256.  Bound: latency (launch, two barriers, a handful of
-// dependent loads) up to a few megabytes of logits, then HBM.
-//
+// dependent loads) up to a few megabytes of logits, then the instructions of a
+// token's softmax.  Measured (softmax, gradient; in us): T = 8192, E = 8, 4
+// sequences 10.2; T = 32768, E = 256, 16 sequences 26.6 (its logits and gradient
+// take 10.2 at the measured copy bandwidth).  As three launches, with a warp per
+// token: 30 and 64.
 #include "internal.h"
 #include "common.cuh"
 
 namespace moe {
 
 constexpr int kBalThreads = 256;
-constexpr int kBalMaxBlocks = 592;  // 4 per SM
+constexpr int kBalMaxBlocks = 444;  // 3 per SM
 constexpr int kBalPer = 8;          // experts per lane: E <= 256
 constexpr int kBalStarts = 2048;    // sequence borders held in shared memory, else searched in global
 constexpr int kBalHist = 4096;      // (sequence, expert) counters of a block's tokens
@@ -143,8 +146,6 @@ template <int L> MOE_DEVICE float group_max(float v)
 
 // A lane's experts: 8 consecutive ones (rows of a multiple of 4: two 16-byte
 // vectors), or every L-th.
-template <int L, bool VEC> MOE_DEVICE int bal_expert(int lg, int j) { return VEC ? lg * kBalPer + j : lg + L * j; }
-
 template <int L, bool VEC, typename V>
 MOE_DEVICE void bal_load(const V* row, int lg, int E, V (&v)[kBalPer], V pad)
 {
@@ -190,12 +191,15 @@ MOE_DEVICE void bal_store(float* row, int lg, int E, const float (&v)[kBalPer])
     }
 }
 
-template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) balance_kernel(const BalArgs a)
+template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) balance_kernel(const BalArgs a)
 {
     __shared__ BalShared sh;
     const int tid = threadIdx.x, E = a.E;
     const int64_t gtid = (int64_t)blockIdx.x * kBalThreads + tid, gstep = (int64_t)gridDim.x * kBalThreads;
     const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = t0 + a.chunk < a.T ? t0 + a.chunk : a.T;
+    int first_id[8];  // the ids of the thread's first token (K <= 8), on their way from here
+#pragma unroll
+    for (int k = 0; k < 8; ++k) first_id[k] = t0 + tid < t1 && k < a.K ? a.ids[(t0 + tid) * a.K + k] : 0;
     // zero this call's sums, then check the borders
     for (int64_t k = gtid; k < a.S; k += gstep) {
         a.w.tokens[k] = 0;
@@ -215,8 +219,6 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
         for (int i = tid; i <= a.S; i += kBalThreads) sh.starts[i] = a.starts[i];
         starts = sh.starts;
     }
-    for (int i = tid; i < kBalHist; i += kBalThreads) sh.hist[i] = 0;
-    for (int i = tid; i < kBalSpan; i += kBalThreads) sh.tokens[i] = 0;
     __syncthreads();
     if (tid == 0) sh.lo = bal_find(starts, a.S, t0);
     if (tid == 32) sh.hi = bal_find(starts, a.S, t1 - 1);
@@ -225,9 +227,9 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
     const bool local = span >= 1 && span <= kBalSpan && (int64_t)span * E <= kBalHist;
     auto count = [&](bool in_shared) {
         for (int64_t t = t0 + tid; t < t1; t += kBalThreads) {
-            int id[8];  // K <= 8; on their way while the sequence is looked up
+            int id[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) id[k] = k < a.K ? a.ids[t * a.K + k] : 0;
+            for (int k = 0; k < 8; ++k) id[k] = t == t0 + tid ? first_id[k] : k < a.K ? a.ids[t * a.K + k] : 0;
             const int i = bal_sequence(a, starts, t);
             if (i < 0) continue;
             const bool here = in_shared && i >= lo && i < lo + span;
@@ -244,8 +246,11 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
     // borders that do not rise can put a token outside lo .. hi: those blocks count
     // in global memory like the ones whose sequences do not fit
     bool rising = true;
-    if (local)
+    if (local) {
+        for (int i = tid; i < span * E; i += kBalThreads) sh.hist[i] = 0;
+        for (int i = tid; i < span; i += kBalThreads) sh.tokens[i] = 0;
         for (int i = lo + tid; i < lo + span && i < a.S; i += kBalThreads) rising &= starts[i] <= starts[i + 1];
+    }
     const bool in_shared = __syncthreads_and(local && rising) != 0;
     if (in_shared) count(true);
     bal_wait(a, 1);  // the sums are zero everywhere
@@ -268,6 +273,8 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
     const int lg = tid & (L - 1);
     const int64_t per = kBalThreads / L;
     float nl[kBalPer], f[kBalPer];
+#pragma unroll
+    for (int j = 0; j < kBalPer; ++j) nl[j] = f[j] = 0.f;
     int ni = -1, at = -1, i_of = -1;  // the next token's sequence; where it was found; the one f is of
     auto fetch = [&](int64_t t) {
         ni = -1;
@@ -317,10 +324,19 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kBalPer; ++j) {
-            l[j] = i >= 0 ? nl[j] : 0.f;
+            l[j] = nl[j];
             mx = fmaxf(mx, l[j]);
         }
         if (base + per < t1) fetch(t + per);
+        if (L == 32 && i < 0) {  // the whole warp's token does not count
+            if (a.dlogits != nullptr) {
+                float d[kBalPer];
+#pragma unroll
+                for (int j = 0; j < kBalPer; ++j) d[j] = 0.f;
+                bal_store<L, VEC>(a.dlogits + t * E, lg, E, d);
+            }
+            continue;
+        }
         if (i >= 0 && i != i_of) {
             if (acc != 0) atomicAdd(&a.w.acc[i_of], acc);
             acc = 0;
@@ -339,11 +355,10 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
         float se = 0.f, sg = 0.f, one_less[kBalPer];
 #pragma unroll
         for (int j = 0; j < kBalPer; ++j) {
-            const bool in = bal_expert<L, VEC>(lg, j) < E;
-            p[j] = in ? __expf(l[j] - mx) : 0.f;
+            p[j] = __expf(l[j] - mx);  // 0 for the lanes' places behind E, which hold -inf
             se += p[j];
             if (a.sigmoid) {
-                const float sc = in ? __fdividef(1.f, 1.f + __expf(-l[j])) : 0.f;
+                const float sc = __fdividef(1.f, 1.f + __expf(-l[j]));
                 l[j] = sc;
                 one_less[j] = 1.f - sc;
                 sg += sc;
@@ -360,7 +375,7 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
 #pragma unroll
         for (int j = 0; j < kBalPer; ++j) {
             p[j] *= inv_se;
-            c += i >= 0 ? f[j] * (a.sigmoid ? l[j] : p[j]) : 0.f;
+            c = fmaf(f[j], a.sigmoid ? l[j] : p[j], c);
         }
         c = group_sum<L>(c);
         if (t >= t1) continue;
@@ -392,26 +407,27 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 4) bal
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if ((tid & 31) == 0) sh.red[0][tid >> 5] = z;
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
         double s = 0.0;
         for (int w = 0; w < kBalThreads / 32; ++w) s += sh.red[0][w];
         a.w.zpart[blockIdx.x] = s;
-        __threadfence();
-        sh.last = atomicAdd(a.w.done, 1u) == gridDim.x - 1;
+        // releases this block's additions (thread 0's release covers what the block
+        // barrier ordered before it) and acquires the others'
+        uint32_t n;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(a.w.done) : "memory");
+        sh.last = n == gridDim.x - 1;
     }
     __syncthreads();
     if (!sh.last) return;
-    __threadfence();
     // the block that finishes last: per-sequence losses, then both means
     double zsum = 0.0, bsum = 0.0;
     for (int64_t b = tid; b < gridDim.x; b += kBalThreads) zsum += __ldcg(&a.w.zpart[b]);
     for (int64_t k = tid; k < a.S; k += kBalThreads) {
-        const int n = __ldcg(&a.w.tokens[k]);
+        const int n = __ldcg(&a.w.tokens[k]), bad = __ldcg(&a.w.bad[k]);
+        const unsigned long long sum = __ldcg(&a.w.acc[k]);
         double v = 0.0;
-        if (n > 0)
-            v = __ldcg(&a.w.bad[k]) ? (double)NAN : (double)E * ((double)__ldcg(&a.w.acc[k]) / kBalFix) / (double)n;
+        if (n > 0) v = bad ? (double)NAN : (double)E * (1.0 / kBalFix) * (double)sum / (double)n;
         a.seq_loss[k] = (float)v;
         bsum += v;
     }
