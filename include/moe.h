@@ -485,7 +485,9 @@ MOE_API moe_status moe_mx8_workspace_size(const moe_config *cfg, size_t *bytes);
  * (max_rows, F) and hs (max_rows, F / 32): the intermediate, written here.
  * hq and y_perm start on a 32-byte boundary (MOE_ERR_ALIGN otherwise).
  * perm and topk_w may both be NULL (weight 1).  Rows at and behind offsets[E]
- * are left as they were.  A NaN scale makes the rows that meet it NaN.
+ * are left as they were.  A NaN scale makes the rows that meet it NaN.  Offsets
+ * that decrease or leave 0 .. max_rows anywhere: nothing is computed, and the
+ * bounds flag is raised; a perm entry out of range: weight 0, and the flag.
  */
 MOE_API moe_status moe_expert_ffn_mx8(const moe_config *cfg, const void *xq, const void *xs,
                                       const int32_t *offsets, const int32_t *perm, const float *topk_w,

@@ -70,13 +70,17 @@ constexpr int MAX_E = 256;
 // 101 and 105, 32 rows 105 and 104, 48 rows 121 and 106.
 constexpr int kFewRows = 24;
 
-template <bool PAIR> struct Geo {
+template <bool GATEUP, bool PAIR> struct Geo {
     static constexpr int CTAS = PAIR ? 2 : 1;
     static constexpr int BM = 128 * CTAS;
     static constexpr int B_ROWS = 256 / CTAS;              // rows of B in this CTA
     static constexpr int B_BYTES = B_ROWS * BK;
     static constexpr int OP_BYTES = A_BYTES + B_BYTES;     // one stage's operands
-    static constexpr int STAGES = PAIR ? 6 : 4;
+    // a pair's down product gives one operand stage for 64-column pieces of y, 4 KB
+    // per epilogue warp, that leave by TMA in whole lines
+    static constexpr bool STAGED = PAIR && !GATEUP;
+    static constexpr int OUT_BYTES = STAGED ? 4096 : 0;
+    static constexpr int STAGES = STAGED ? 5 : PAIR ? 6 : 4;
 };
 
 struct Misc {
@@ -96,9 +100,10 @@ struct Misc {
     int warp_sum[NUM_THREADS / 32];
 };
 
-template <bool PAIR> constexpr size_t smem_bytes()
+template <bool GATEUP, bool PAIR> constexpr size_t smem_bytes()
 {
-    return 1024 + (size_t)Geo<PAIR>::STAGES * Geo<PAIR>::OP_BYTES + SF_SLOTS * SF_SLOT_BYTES + sizeof(Misc);
+    using G = Geo<GATEUP, PAIR>;
+    return 1024 + (size_t)G::STAGES * G::OP_BYTES + EPI_WARPS * G::OUT_BYTES + SF_SLOTS * SF_SLOT_BYTES + sizeof(Misc);
 }
 
 struct Args {
@@ -295,14 +300,15 @@ MOE_DEVICE float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-
 template <bool GATEUP, bool PAIR>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     ffn_mx8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                   const __grid_constant__ CUtensorMap tmB1, const Args a)
+                   const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
-    using G = Geo<PAIR>;
+    using G = Geo<GATEUP, PAIR>;
     constexpr int BM = G::BM, BN = GATEUP ? 128 : 256, STAGES = G::STAGES, OP_BYTES = G::OP_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stages = smem;
-    uint8_t* scales = smem + (size_t)STAGES * OP_BYTES;
+    uint8_t* outbuf = smem + (size_t)STAGES * OP_BYTES;  // EPI_WARPS x OUT_BYTES, 1 KB aligned
+    uint8_t* scales = outbuf + (size_t)EPI_WARPS * G::OUT_BYTES;
     Misc* m = reinterpret_cast<Misc*>(scales + (size_t)SF_SLOTS * SF_SLOT_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = a.E;
@@ -330,6 +336,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB0);
         if (GATEUP) prefetch_tmap(&tmB1);
+        if (G::STAGED) prefetch_tmap(&tmY);
     }
     if (warp == 1) {
         if (PAIR) {
@@ -598,6 +605,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t tempty0 = mapa_shared(smem_u32(&m->tempty[0]), 0);
         const uint32_t tempty1 = mapa_shared(smem_u32(&m->tempty[1]), 0);
         const uint32_t tover = mapa_shared(smem_u32(&m->tover), 0);
+        uint8_t* obuf = outbuf + (size_t)(warp - EPI_WARP0) * G::OUT_BYTES;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int t = unit; t < total; t += units) {
@@ -614,6 +622,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if (!warp_wait(&m->tfull[acc], acc_phase, lane, a.status, 730, abort_flag)) break;
             tc_fence_after();
+            // the warp's 32 rows all belong to the expert: its pieces leave by TMA
+            const int64_t warp_row0 = (int64_t)m_row0 + (int)rank * 128 + quad * 32;
+            const bool staged = G::STAGED && warp_row0 + 32 <= row_end;
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * ACC_STRIDE);
             // the shared columns: the last 32 of accumulator 0, the first 32 of 1
             const bool shared_half = half == (acc == 0 ? 1 : 0);
@@ -639,6 +650,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         else mbar_arrive(&m->tover);
                     }
                 }
+                if (staged && (cc & 1) == 0) {  // the last piece has been read
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+                }
                 if (GATEUP) {
                     if (valid && col < a.N) {
                         uint32_t mx = 0;
@@ -663,9 +678,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         p[j] = pack_bf16x2(w * __uint_as_float(v[2 * j]), w * __uint_as_float(v[2 * j + 1]));
-                    if (valid) {
-                        store32(a.y + row * a.N + col, p);
-                        store32(a.y + row * a.N + col + 16, p + 8);
+                    if (!staged) {
+                        if (valid) {
+                            store32(a.y + row * a.N + col, p);
+                            store32(a.y + row * a.N + col + 16, p + 8);
+                        }
+                    } else {
+                        // half a row of the piece (128-byte swizzle: 16-byte part q of row r at
+                        // part q ^ (r & 7))
+                        uint4* dst = reinterpret_cast<uint4*>(obuf + lane * 128);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dst[((c & 1) * 4 + q) ^ (lane & 7)] =
+                                make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+                    }
+                }
+                if (staged && (cc & 1) == 1 && (col & ~63) < a.N) {  // columns past N fall outside the map
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmY, obuf, col & ~63, (int)warp_row0);
+                        bulk_commit();
                     }
                 }
             }
@@ -679,6 +712,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 acc = 0;
                 acc_phase ^= 1u;
             }
+        }
+        if (G::STAGED) {
+            if (lane == 0) bulk_wait_all<0>();  // every store of this warp has completed
+            __syncwarp();
         }
     }
     tc_fence_before();
@@ -1079,6 +1116,21 @@ static bool map_bytes(CUtensorMap* m, const void* base, uint64_t K, uint64_t row
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// y (rows, cols) bf16 for stores of 32 rows x 64 columns from shared memory laid out
+// with the 128-byte swizzle.
+static bool map_store(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows)
+{
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols * 2};
+    cuuint32_t box[2] = {64, 32};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Per device: shared memory opted in, and how many CTAs or pairs are resident.
 template <bool GATEUP, bool PAIR> static cudaError_t prepare(int* resident)
 {
@@ -1093,7 +1145,7 @@ template <bool GATEUP, bool PAIR> static cudaError_t prepare(int* resident)
             return cudaSuccess;
         }
     }
-    constexpr size_t smem = smem_bytes<PAIR>();
+    constexpr size_t smem = smem_bytes<GATEUP, PAIR>();
     e = cudaFuncSetAttribute(ffn_mx8_kernel<GATEUP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     int units = 0;
@@ -1122,7 +1174,7 @@ template <bool GATEUP, bool PAIR> static cudaError_t prepare(int* resident)
 
 template <bool GATEUP, bool PAIR>
 static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, const CUtensorMap& mB1,
-                              const Args& a, int64_t tiles_bound, cudaStream_t s)
+                              const CUtensorMap& mY, const Args& a, int64_t tiles_bound, cudaStream_t s)
 {
     int units = 0;
     cudaError_t e = prepare<GATEUP, PAIR>(&units);
@@ -1144,13 +1196,13 @@ static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, con
         attr[na].val.programmaticStreamSerializationAllowed = 1;
         ++na;
     }
-    cfg.gridDim = dim3((unsigned)(Geo<PAIR>::CTAS * n), 1, 1);
+    cfg.gridDim = dim3((unsigned)(Geo<GATEUP, PAIR>::CTAS * n), 1, 1);
     cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem_bytes<PAIR>();
+    cfg.dynamicSmemBytes = smem_bytes<GATEUP, PAIR>();
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, PAIR>, mA, mB0, mB1, a);
+    return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, PAIR>, mA, mB0, mB1, mY, a);
 }
 
 template <bool GATEUP, int NT>
@@ -1196,7 +1248,7 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
     d.as = u8(hs); d.b0s = d.b1s = u8(w.down_scales);
     d.y = static_cast<__nv_bfloat16*>(y_perm);
     d.Kdim = c.F; d.N = c.D; d.n_tiles = (c.D + 255) / 256;
-    CUtensorMap mX, mG, mU, mH, mD;
+    CUtensorMap mX, mG, mU, mH, mD, mY;
     if (max_rows <= kFewRows * (int64_t)c.E) {
         constexpr int NT = 32;
         if (!map_bytes(&mX, xq, D, R, 0, NT) || !map_bytes(&mG, w.gate, D, F, E, 128) ||
@@ -1209,7 +1261,7 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
     }
     if (!map_bytes(&mX, xq, D, R, 0, 128) || !map_bytes(&mG, w.gate, D, F, E, 64) ||
         !map_bytes(&mU, w.up, D, F, E, 64) || !map_bytes(&mH, hq, F, R, 0, 128) ||
-        !map_bytes(&mD, w.down, F, D, E, 64))
+        !map_bytes(&mD, w.down, F, D, E, 64) || !map_store(&mY, y_perm, D, R))
         return cudaErrorInvalidValue;
     // CTA pairs when experts hold 128 rows or more on average, as the bf16
     // experts: single CTAs waste fewer padded rows on a few tokens each
@@ -1226,11 +1278,11 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
     }
     a.amaps = gm;
     d.amaps = gm ? gm + c.E : nullptr;
-    cudaError_t e = pair ? launch_one<true, true>(mX, mG, mU, a, mt * a.n_tiles, s)
-                         : launch_one<true, false>(mX, mG, mU, a, mt * a.n_tiles, s);
+    cudaError_t e = pair ? launch_one<true, true>(mX, mG, mU, mY, a, mt * a.n_tiles, s)
+                         : launch_one<true, false>(mX, mG, mU, mY, a, mt * a.n_tiles, s);
     if (e != cudaSuccess) return e;
-    return pair ? launch_one<false, true>(mH, mD, mD, d, mt * d.n_tiles, s)
-                : launch_one<false, false>(mH, mD, mD, d, mt * d.n_tiles, s);
+    return pair ? launch_one<false, true>(mH, mD, mD, mY, d, mt * d.n_tiles, s)
+                : launch_one<false, false>(mH, mD, mD, mY, d, mt * d.n_tiles, s);
 }
 
 }  // namespace moe

@@ -454,45 +454,52 @@ def test_experts_mx8(case):
     assert torch.equal(y, y2) and torch.equal(hq, hq2) and torch.equal(hs, hs2)
 
 
-def test_experts_mx8_unit_weights_and_unused_rows():
+@pytest.mark.parametrize("T,E,counts", [(100, 3, [70, 0, 50]), (40, 6, [0, 33, 1, 0, 6, 0]), (400, 3, [300, 0, 129])])
+def test_experts_mx8_unit_weights_and_unused_rows(T, E, counts):
     """Weight 1 without perm; rows behind offsets[E] stay as they were."""
-    st = _experts_state(100, 128, 96, 3, 2, 9, counts=[70, 0, 50])  # 120 of 200 rows
+    st = _experts_state(T, 128, 96, E, 2, 9, counts=counts)  # fewer than the 2 T rows there are
+    used = sum(counts)
     hq, hs, y, ws = _run_experts(st, weighted=False)
     assert B.moe_get_device_status(ws) == 0
     _check_experts(st, hq, hs, y, weighted=False)
-    assert bool((y[120:] == 7).all()) and bool((hq[120:] == 0x55).all()) and bool((hs[120:] == 0x55).all())
-    none = _experts_state(4, 64, 64, 2, 2, 9, counts=[0, 0])
+    assert bool((y[used:] == 7).all()) and bool((hq[used:] == 0x55).all()) and bool((hs[used:] == 0x55).all())
+    none = _experts_state(T, 64, 64, E, 2, 9, counts=[0] * E)
     hq, hs, y, ws = _run_experts(none)
     assert B.moe_get_device_status(ws) == 0 and bool((y == 7).all()) and bool((hq == 0x55).all())
 
 
-def test_experts_mx8_faults_are_seen():
-    """A NaN scale makes its row NaN and no other; malformed offsets and perm
-    entries raise the bounds flag."""
-    st = _experts_state(50, 256, 128, 2, 1, 4)
+@pytest.mark.parametrize("T,E", [(50, 2), (50, 8), (300, 2)])  # single CTAs, few rows, CTA pairs
+def test_experts_mx8_faults_are_seen(T, E):
+    """A NaN scale makes its row NaN and no other; malformed offsets compute nothing
+    and raise the bounds flag, as does a perm entry out of range."""
+    st = _experts_state(T, 256, 128, E, 1, 4)
     _, _, y0, _ = _run_experts(st)
     st["xs"] = st["xs"].clone()
     st["xs"][17, 3] = 255
     _, hs, y, _ = _run_experts(st)
     assert bool(y[17].isnan().all()) and bool((hs[17] == 255).all())
-    keep = [r for r in range(50) if r != 17]
+    keep = [r for r in range(T) if r != 17]
     assert torch.equal(y[keep], y0[keep])
-    st = _experts_state(50, 256, 128, 2, 1, 4)
-    for bad in ([0, 20, 51], [0, 30, 20], [-5, 20, 50]):
+    st = _experts_state(T, 256, 128, E, 1, 4)
+    good = st["offsets"].tolist()
+    for bad in (good[:-1] + [T + 1], good[:1] + [T - 1] + good[1:-1], [-5] + good[1:]):
         st2 = dict(st, offsets=torch.tensor(bad, dtype=torch.int32, device="cuda"))
-        _, _, _, ws = _run_experts(st2)
+        _, _, y, ws = _run_experts(st2)
         assert B.moe_get_device_status(ws) == B.MOE_DEVFLAG_BOUNDS
-    for bad in (-1, 50):
+        assert bool((y == 7).all())
+    for bad in (-1, T):
         p = st["perm"].clone()
         p[7] = bad
-        _, _, _, ws = _run_experts(dict(st, perm=p))
+        _, _, y, ws = _run_experts(dict(st, perm=p))
         assert B.moe_get_device_status(ws) == B.MOE_DEVFLAG_BOUNDS
+        assert torch.equal(y[8:], y0[8:]) and bool((y[7] == 0).all())
     _, _, y, ws = _run_experts(st)
     assert B.moe_get_device_status(ws) == 0 and torch.equal(y, y0)
 
 
-def test_experts_mx8_on_another_stream_and_in_a_graph():
-    st = _experts_state(200, 256, 192, 4, 2, 21)
+@pytest.mark.parametrize("T,E", [(200, 4), (30, 8), (400, 2)])
+def test_experts_mx8_on_another_stream_and_in_a_graph(T, E):
+    st = _experts_state(T, 256, 192, E, 2, 21)
     hq, hs, y0, _ = _run_experts(st)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
