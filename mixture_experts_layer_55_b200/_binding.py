@@ -342,6 +342,10 @@ def moe_backward(cfg, x, w_router, w_gate, w_up, w_down, state, dy, dx, dw_route
     """shared = (w_gate_s, w_up_s, w_down_s) and dshared = their fp32
     gradient buffers when cfg.F_shared > 0.  dlogits_add (T, E) fp32: a further
     gradient of the routing logits (moe_balance_loss's)."""
+    if dlogits_add is not None:
+        import torch
+        if dlogits_add.dtype != torch.float32 or dlogits_add.numel() != cfg.T * cfg.E:
+            raise ValueError("moe_backward: dlogits_add must be (T, E) fp32")
     sg, su, sd = shared if shared is not None else (None, None, None)
     dg, du, dd = dshared if dshared is not None else (None, None, None)
     st = lib().moe_backward_aux(_cfg(cfg), _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up),
@@ -504,6 +508,14 @@ def _types():
     return _TYPES
 
 
+def _ws(where, workspace):
+    """The workspace's _check_tensors entry: any number of bytes (the library says
+    whether they are enough)."""
+    if workspace is None:
+        raise ValueError(f"{where}: workspace must be a tensor")
+    return "workspace", workspace, _types()[4], workspace.numel()
+
+
 def _rows(where, name, t, layer):
     if getattr(t, "dim", None) is None or t.dim() != 2 or t.dtype not in layer:
         raise ValueError(f"{where}: {name} must be a (rows, columns) bf16 or fp32 tensor")
@@ -542,7 +554,7 @@ def moe_rmsnorm_backward(dn, s, gamma, rstd, dx, dgamma, workspace, ds=None, str
     dev, p = _check_tensors("moe_rmsnorm_backward", (
         ("s", s, dt, nel), ("dn", dn, dt, nel), ("gamma", gamma, f32, D), ("rstd", rstd, f32, T),
         ("dx", dx, dt, nel), ("dgamma", dgamma, f32, D), ("ds", ds, dt, nel),
-        ("workspace", workspace, byte, workspace.numel())))
+        _ws("moe_rmsnorm_backward", workspace)))
     _run("moe_rmsnorm_backward", dev, lib().moe_rmsnorm_backward,
          (T, D, layer[s.dtype], p[1], p[6], p[0], p[2], p[3], p[4], p[5], p[7], workspace.numel()), stream)
 
@@ -611,7 +623,7 @@ def moe_expert_ffn_mx8(cfg, xq, xs, offsets, perm, topk_w, weights, hq, hs, y_pe
         ("xq", xq, q8, R * cfg.D), ("xs", xs, byte, R * cfg.D // 32), ("offsets", offsets, i32, cfg.E + 1),
         ("perm", perm, i32, R), ("topk_w", topk_w, f32, cfg.T * cfg.K), ("hq", hq, q8, R * cfg.F),
         ("hs", hs, byte, R * cfg.F // 32), ("y_perm", y_perm, (torch.bfloat16,), R * cfg.D),
-        ("workspace", workspace, byte, workspace.numel())] + _mx8_specs(cfg, weights))
+        _ws("moe_expert_ffn_mx8", workspace)] + _mx8_specs(cfg, weights))
     w = Mx8Weights(*p[9:])
     _run("moe_expert_ffn_mx8", dev, lib().moe_expert_ffn_mx8,
          (_cfg(cfg), *p[:5], ctypes.byref(w), *p[5:9], workspace.numel()), stream)
@@ -638,7 +650,7 @@ def moe_forward_mx8(cfg, x, w_router, weights, y, workspace, xq=None, xs=None, y
         ("selection_bias", selection_bias, f32, E), ("logit_noise", logit_noise, f32, T * E),
         ("w_router_terms", w_router_terms, byte, router_terms_size(cfg)), ("losses", losses, f32, 3),
         ("mean_prob", mean_prob, f32, E), ("counts", counts, i32, E), ("topk_ids", topk_ids, i32, T * K),
-        ("topk_w", topk_w, f32, T * K), ("workspace", workspace, byte, workspace.numel())]
+        ("topk_w", topk_w, f32, T * K), _ws("moe_forward_mx8", workspace)]
         + _mx8_specs(cfg, weights))
     w = Mx8Weights(*p[16:])
     _run("moe_forward_mx8", dev, lib().moe_forward_mx8,
@@ -665,7 +677,7 @@ def moe_balance_loss(cfg, logits, topk_ids, seq_starts, counts, losses, seq_loss
         ("logits", logits, f32, T * E), ("topk_ids", topk_ids, i32, T * cfg.K),
         ("seq_starts", seq_starts, i32, S + 1), ("counts", counts, i32, S * E), ("losses", losses, f32, 2),
         ("seq_loss", seq_loss, f32, S), ("token_mask", token_mask, byte, T), ("dlogits", dlogits, f32, T * E),
-        ("workspace", workspace, byte, workspace.numel())))
+        _ws("moe_balance_loss", workspace)))
     _run("moe_balance_loss", dev, lib().moe_balance_loss,
          (_cfg(cfg), S, p[0], p[1], p[2], p[6], c_balance, c_z, p[3], p[4], p[5], p[7], p[8],
           workspace.numel()), stream)

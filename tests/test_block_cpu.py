@@ -185,6 +185,46 @@ def test_binding_checks_tensors(lib):
                            torch.zeros(1), torch.zeros(256, dtype=torch.uint8))
 
 
+def test_binding_refuses_missing_workspace_and_wrong_gradient(lib):
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="workspace"):
+        B.moe_rmsnorm_backward(x, x, torch.ones(64), torch.ones(4), x, torch.ones(64), None)
+    c = _cfg(T=4)
+    for bad in (torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(4, 7)):
+        with pytest.raises(ValueError, match="dlogits_add"):
+            B.moe_backward(c, *([None] * 13), dlogits_add=bad)
+
+
+def test_calls_go_to_the_tensors_device(monkeypatch):
+    """Tensors on a device that is not the current one: the call is made with that
+    device current and on its current stream, and the current device comes back."""
+    log, current = [], [0]
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.d
+
+        def __exit__(self, *a):
+            current[0] = self.old
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+
+    def fn(*args):
+        log.append((current[0], args))
+        return B.MOE_OK
+    B._run("x", 0, fn, (1, 2), None)
+    B._run("x", 3, fn, (1, 2), None)
+    B._run("x", 3, fn, (1, 2), 77)
+    assert log == [(0, (1, 2, 1000)), (3, (1, 2, 1003)), (3, (1, 2, 77))] and current == [0]
+    with pytest.raises(B.MoEError):
+        B._run("x", 0, lambda *a: B.MOE_ERR_ARG, (), None)
+
+
 def test_layer_refuses(lib):
     """8-bit experts with a shared expert, an unknown kind of experts."""
     w = [torch.zeros(2, 64, 64, dtype=torch.bfloat16) for _ in range(3)]
