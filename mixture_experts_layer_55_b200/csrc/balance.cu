@@ -328,8 +328,8 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) bal
             mx = fmaxf(mx, l[j]);
         }
         if (base + per < t1) fetch(t + per);
-        if (L == 32 && i < 0) {  // the whole warp's token does not count
-            if (a.dlogits != nullptr) {
+        if (L == 32 && i < 0) {  // the whole warp's token does not count, or is behind the chunk
+            if (t < t1 && a.dlogits != nullptr) {
                 float d[kBalPer];
 #pragma unroll
                 for (int j = 0; j < kBalPer; ++j) d[j] = 0.f;

@@ -330,6 +330,45 @@ def test_balance_loss(case, score):
     assert torch.equal(c2, counts) and torch.equal(l2, losses) and torch.equal(s2, seq)
 
 
+@pytest.mark.parametrize("T,E,K,S,masked", [(32771, 256, 8, 16, True), (30001, 130, 3, 7, False), (65537, 64, 6, 300, True),
+                                            (140000, 8, 2, 3, True), (40003, 33, 2, 5, True), (70001, 17, 1, 9, False)])
+def test_balance_loss_many_tokens(T, E, K, S, masked):
+    """Batches whose blocks take several rounds of tokens each, the last one
+    ragged: every gradient row, and nothing written around the outputs."""
+    g = _gen(T)
+    logits, ids = _randn(g, T, E), _ids(g, T, E, K)
+    cuts = torch.sort(torch.randint(0, T + 1, (S,), generator=g, device="cuda")).values.tolist()
+    starts = [0] + cuts
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.7).to(torch.uint8) if masked else None
+    cfg = M.MoeConfig.make(T, 8, 8, E, K, "bf16")
+    ws = torch.zeros(M.balance_workspace_size(cfg, S), dtype=torch.uint8, device="cuda")
+    pad = 4096  # a multiple of 16 bytes around every output
+    bufs = [torch.full((n + 2 * pad,), 77, dtype=dt, device="cuda") for n, dt in
+            ((S * E, torch.int32), (2, torch.float32), (S, torch.float32), (T * E, torch.float32))]
+    counts, losses, seq, d = (b[pad:-pad] for b in bufs)
+    M.moe_balance_loss(cfg, logits, ids, torch.tensor(starts, dtype=torch.int32, device="cuda"), counts, losses, seq,
+                       ws, token_mask=mask, dlogits=d, c_balance=0.01, c_z=0.001)
+    assert B.moe_get_device_status(ws) == 0
+    for b in bufs:
+        assert bool((b[:pad] == 77).all()) and bool((b[-pad:] == 77).all())
+    rc, rs, rd, rz, rb = _balance_ref(logits, ids, starts, mask, "softmax", 0.01, 0.001)
+    assert torch.equal(counts.reshape(S, E).long(), rc)
+    tol = 2.0**-18
+    _within(seq, rs, tol * rs + E * 2.0**-33, "seq_loss")
+    assert abs(float(losses[0]) - rz) <= tol * rz and abs(float(losses[1]) - rb) <= tol * rb + E * 2.0**-33
+    # the gradient's two parts, as above
+    on = torch.ones(T, dtype=torch.float64, device="cuda") if mask is None else (mask != 0).double()
+    n, total = torch.zeros(T, dtype=torch.float64, device="cuda"), 0.0
+    for a, b in zip(starts[:-1], starts[1:]):
+        n[a:b] = 1 / on[a:b].sum().clamp(min=1)
+        total += float(on[a:b].sum())
+    l64 = logits.double()
+    p, lse = torch.softmax(l64, 1), torch.logsumexp(l64, 1).abs()
+    used = max(1, int((rs > 0).sum()))
+    bound = 2 * 0.01 * E / used * n[:, None] * p + 2 * 0.001 * lse[:, None] * p / max(1.0, total)
+    _within(d.reshape(T, E), rd, tol * bound + 1e-30, "dlogits")
+
+
 def test_balance_gradient_against_differences():
     g = _gen(5)
     T, E, K, starts = 60, 12, 3, [0, 25, 25, 55]
