@@ -101,6 +101,62 @@ def test_rmsnorm(T, D, dt, residual, bits8):
     assert torch.equal(x2, n) and (not residual or torch.equal(r2, s))
 
 
+# many rows a team, all widths' forms; the last rows ragged
+MANY = [(20003, 64, "bf16"), (20001, 96, "f32"), (9001, 512, "f32"), (9001, 512, "bf16"), (5003, 1000, "bf16"),
+        (6001, 1024, "f32"), (4003, 2048, "bf16"), (2501, 4096, "f32"), (1801, 7168, "bf16"), (1201, 8192, "f32"),
+        (900, 12288, "bf16"), (700, 16384, "f32")]
+
+
+@pytest.mark.parametrize("T,D,dt", MANY)
+def test_rmsnorm_many_rows(T, D, dt):
+    """Forward (with a residual and, where D allows, the 8-bit output) and backward of
+    more rows than there are teams, and nothing written around the outputs."""
+    dtype, pad = DT[dt], 4096
+    g = _gen(T + D)
+
+    def out(n, t):
+        b = torch.full((n + 2 * pad,), 77, dtype=torch.uint8, device="cuda") if t == torch.uint8 else \
+            torch.full((n + 2 * pad,), 77.0, dtype=t, device="cuda")
+        bufs.append(b)
+        return b[pad:-pad]
+    bufs = []
+    x, res = _randn(g, T, D, dtype=dtype), _randn(g, T, D, dtype=dtype)
+    gamma = 1 + 0.3 * _randn(g, D)
+    n, s, rstd = out(T * D, dtype).view(T, D), out(T * D, dtype).view(T, D), out(T, torch.float32)
+    q, qs = (out(T * D, torch.uint8), out(T * D // 32, torch.uint8)) if D % 32 == 0 else (None, None)
+    M.moe_rmsnorm(x, gamma, n, residual=res, s=s, rstd=rstd, q=q, q_scales=qs, eps=1e-5)
+    assert torch.equal(s, (x.float() + res.float()).to(dtype))
+    for a in range(0, T, 2048):
+        at = slice(a, a + 2048)
+        s64 = s[at].double()
+        r = (s64.square().mean(1) + 1e-5).rsqrt()
+        _within(rstd[at], r, SUM * r, "rstd")
+        ref = s64 * r[:, None] * gamma.double()
+        _within(n[at], ref, (ROUND[dtype] + SUM) * ref.abs() + 1e-38, "n")
+        if q is not None:
+            rq, rs = _quantize_ref(n[at])
+            assert torch.equal(qs.view(T, -1)[at], rs)
+            assert torch.equal(_value(q.view(T, D)[at], qs.view(T, -1)[at]), _value(rq, rs))
+    dn, ds = _randn(g, T, D, dtype=dtype), _randn(g, T, D, dtype=dtype)
+    dx, dg = out(T * D, dtype).view(T, D), out(D, torch.float32)
+    ws = torch.zeros(M.rmsnorm_backward_workspace_size(T, D), dtype=torch.uint8, device="cuda")
+    M.moe_rmsnorm_backward(dn, s, gamma, rstd, dx, dg, ws, ds=ds)
+    dgr, dgm = torch.zeros(D, dtype=torch.float64, device="cuda"), torch.zeros(D, dtype=torch.float64, device="cuda")
+    for a in range(0, T, 2048):
+        at = slice(a, a + 2048)
+        r, dn64 = rstd[at].double()[:, None], dn[at].double()
+        xh, gg = s[at].double() * r, dn64 * gamma.double()
+        mean, mag = (gg * xh).mean(1, keepdim=True), (gg * xh).abs().mean(1, keepdim=True)
+        ref = r * (gg - xh * mean) + ds[at].double()
+        parts = r * (gg.abs() + xh.abs() * mag) + ds[at].double().abs()
+        _within(dx[at], ref, ROUND[dtype] * ref.abs() + SUM * parts, "dx")
+        dgr += (dn64 * xh).sum(0)
+        dgm += (dn64 * xh).abs().sum(0)
+    _within(dg, dgr, SUM * dgm, "dgamma")
+    for b in bufs:
+        assert bool((b[:pad] == 77).all()) and bool((b[-pad:] == 77).all())
+
+
 def test_rmsnorm_rows_that_are_not_numbers():
     """An infinity or NaN stays in its row and shows in its 8-bit block; a row of
     zeros is zeros."""
@@ -479,7 +535,9 @@ EXPERTS = [(1, 32, 32, 1, 1, None), (1, 256, 512, 8, 2, None), (3, 96, 160, 2, 2
            (40, 224, 288, 3, 2, [79, 0, 1]), (129, 256, 96, 1, 1, None), (300, 128, 64, 5, 2, [128, 129, 0, 127, 216]),
            (64, 512, 1408, 64, 6, None), (1000, 160, 416, 4, 2, [256, 257, 1, 1486]), (700, 1024, 544, 2, 1, [333, 367]),
            (4, 7168, 64, 256, 8, None), (2000, 2048, 256, 8, 2, None), (60, 224, 160, 8, 2, [70, 0, 33, 1, 16, 0, 0, 0]),
-           (20, 1408, 2080, 4, 2, None), (96, 32, 544, 8, 2, [0, 32, 32, 64, 31, 33, 0, 0])]
+           (20, 1408, 2080, 4, 2, None), (96, 32, 544, 8, 2, [0, 32, 32, 64, 31, 33, 0, 0]),
+           # several tiles a CTA in each form (pairs, single CTAs, few rows)
+           (1500, 256, 2816, 8, 2, None), (200, 128, 4096, 8, 2, None), (150, 4096, 1536, 24, 3, None)]
 
 
 @pytest.mark.parametrize("case", range(len(EXPERTS)))
