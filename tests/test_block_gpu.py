@@ -495,12 +495,16 @@ def _experts_state(T, D, F, E, K, seed, counts=None, wscale=0.05):
 def _run_experts(st, weighted=True, sentinel=7.0):
     c = st["cfg"]
     R = c.T * c.K
-    hq = torch.full((R, c.F), 0x55, dtype=torch.uint8, device="cuda")
-    hs = torch.full((R, c.F // 32), 0x55, dtype=torch.uint8, device="cuda")
-    y = torch.full((R, c.D), sentinel, dtype=torch.bfloat16, device="cuda")
+    pad = 64  # rows before and behind each output that nothing may touch
+    full = (torch.full((R + 2 * pad, c.F), 0x55, dtype=torch.uint8, device="cuda"),
+            torch.full((R + 2 * pad, c.F // 32), 0x55, dtype=torch.uint8, device="cuda"),
+            torch.full((R + 2 * pad, c.D), sentinel, dtype=torch.bfloat16, device="cuda"))
+    hq, hs, y = (b[pad:-pad] for b in full)
     ws = torch.zeros(M.mx8_workspace_size(c), dtype=torch.uint8, device="cuda")
     M.moe_expert_ffn_mx8(c, st["xq"], st["xs"], st["offsets"], st["perm"] if weighted else None,
                          st["topk_w"] if weighted else None, st["w"], hq, hs, y, ws)
+    for b, v in zip(full, (0x55, 0x55, sentinel)):
+        assert bool((b[:pad] == v).all()) and bool((b[-pad:] == v).all())
     return hq, hs, y, ws
 
 
