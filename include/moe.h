@@ -417,7 +417,8 @@ MOE_API int32_t moe_backward_kernel_count(const moe_config *cfg);
  * Outputs, each NULL to skip: s (T, D; only with a residual: MOE_ERR_ARG
  * otherwise), n (T, D), rstd (T) fp32, q (T, D bytes) with q_scales
  * (T, D / 32 bytes; both or neither, D a multiple of 32: MOE_ERR_ALIGN
- * otherwise).  n or q is required.  Squares are summed in fp32.  s and n may be
+ * otherwise).  n or q is required.  Squares are summed in fp32, in other units
+ * where they would leave its range.  s and n may be
  * the memory of x or of residual (not each other's).  D <= 65536
  * (MOE_ERR_UNSUPPORTED), T < 2^31.  A row that holds an infinity or NaN gives
  * what the formulas give; no other row is touched by it.

@@ -139,6 +139,19 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
     };
     constexpr bool AHEAD = VPT * MAXT * (int)sizeof(T) <= 4096;  // else the registers are needed
     if (AHEAD && team < a.T) fetch(team);
+    // a row's values times rstd stay below sqrt(D): their products with this thread's
+    // weights are finite where the weights are below 2^100
+    bool gamma_fits = true;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int c = tid + i * tpr;
+        if (c < a.nvec) {
+            float g[8];
+            load_row8<float>(a.gamma + 8 * c, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) gamma_fits = gamma_fits && fabsf(g[j]) < 0x1p100f;
+        }
+    }
     int flip = 0;
     for (int64_t row = team; row < a.T; row += step, flip ^= 1) {
         const int64_t base = row * a.D;
@@ -162,14 +175,41 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
             }
         }
         if (AHEAD && row + step < a.T) fetch(row + step);
+        // rstd as the sum of two fp32 values: fp32's root, and its Newton correction
+        // from the residual 1 - mean r^2, exact but for the last of its roundings.  n
+        // is then the formula's to 2^-24, and what is rounded further, to bf16 and to 8
+        // bits, falls on the formula's side of a border.
+        double sum = row_add_wide(ss, red[flip], a.warps);
+        float eps = a.eps, unit = 1.f;
+        if (!(sum < 0x1p100) || (sum < 0x1p-90 && eps < 0x1p-100f)) {
+            // the squares leave fp32 (or the row holds a NaN): again in units of 2^70 or
+            // 2^-70, the whole team together
+            unit = sum < 1.0 ? 0x1p70f : 0x1p-70f;
+            eps *= unit * unit;
+            float again = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (tid + i * tpr < a.nvec)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float u = v[i][j] * unit;
+                        again = fmaf(u, u, again);
+                    }
+            if (a.warps > 1) __syncthreads();  // the first sum's slots have been read
+            sum = row_add_wide(again, red[flip], a.warps);
+        }
         // rstd as the sum of two fp32 values, from fp32's root and one Newton step in
-        // fp64: n is then the formula's to 2^-24, and what is rounded further, to bf16
-        // and to 8 bits, falls on the formula's side of a border
-        const double mean = row_add_wide(ss, red[flip], a.warps) * a.inv_d + (double)a.eps;
-        const float r0 = rsqrtf((float)mean);
-        const double r2 = (double)r0 * (1.5 - 0.5 * mean * (double)r0 * (double)r0);
-        const bool plain = r0 > 0.f && r0 < INFINITY;  // else r0 says it: zeros without eps, overflow, NaN
-        const float r = plain ? (float)r2 : r0, r_lo = plain ? (float)(r2 - (double)r) : 0.f;
+        // fp64: n is then the formula's rounded to fp32 but for a percent of cases, and
+        // what is rounded further, to bf16 and to 8 bits, falls on the formula's side
+        // of a border (the step in fp32 took the same time and missed a third).
+        const double mean = sum * a.inv_d + (double)eps;
+        const float root = rsqrtf((float)mean);
+        const double fine = (double)root * (1.5 - 0.5 * mean * (double)root * (double)root);
+        // (not where the root says it all: a row of zeros without eps, an overflow, a
+        // NaN; nor where r0's parts leave fp32)
+        const bool carry = gamma_fits && root > 0x1p-60f && root < 0x1p60f;
+        const float near = carry ? (float)fine : root;
+        const float r0 = near * unit, r_lo = carry ? (float)(fine - (double)near) * unit : 0.f, r = r0;
         if (tid == 0 && a.rstd != nullptr) a.rstd[row] = r;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -180,10 +220,13 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
                 load_row8<float>(a.gamma + 8 * c, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {  // v r g with its roundings' errors carried along
-                    const float t = v[i][j] * r, n = t * g[j];
-                    const float et = fmaf(v[i][j], r_lo, fmaf(v[i][j], r, -t));
-                    const float en = fmaf(et, g[j], fmaf(t, g[j], -n));
-                    v[i][j] = isfinite(en) ? n + en : n;
+                    const float t = v[i][j] * r0, n = t * g[j];
+                    if (!carry) {
+                        v[i][j] = n;
+                        continue;
+                    }
+                    const float et = fmaf(v[i][j], r_lo, fmaf(v[i][j], r0, -t));
+                    v[i][j] = n + fmaf(et, g[j], fmaf(t, g[j], -n));
                 }
                 R::store(n_out != nullptr ? n_out + base + 8 * c : nullptr, v[i]);
             }

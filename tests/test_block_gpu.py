@@ -157,6 +157,23 @@ def test_rmsnorm_many_rows(T, D, dt):
         assert bool((b[:pad] == 77).all()) and bool((b[-pad:] == 77).all())
 
 
+@pytest.mark.parametrize("scale,eps", [(1e-18, 0.0), (1e-12, 0.0), (1e15, 0.0), (1e18, 1e-6), (1.0, 1e4), (1e-30, 0.0),
+                                       (1e-25, 1e-12), (1e30, 1e-6), (2e38, 1e-6)])
+def test_rmsnorm_scales(scale, eps):
+    """Rows of very small and very large values (whose squares leave fp32), a large
+    eps, and weights beyond the range the correction is carried in."""
+    g = _gen(77)
+    x = (scale * (0.5 + torch.rand(40, 512, generator=g, device="cuda"))).float()
+    gamma = 1 + 0.3 * _randn(g, 512)
+    gamma[5], gamma[200] = 1e32, -1e33
+    n, rstd = torch.empty_like(x), torch.empty(40, device="cuda")
+    M.moe_rmsnorm(x, gamma, n, rstd=rstd, eps=eps)
+    r = (x.double().square().mean(1) + eps).rsqrt()
+    _within(rstd, r, SUM * r, "rstd")
+    ref = x.double() * r[:, None] * gamma.double()
+    _within(n, ref, (ROUND[torch.float32] + SUM) * ref.abs() + 1e-38, "n")
+
+
 def test_rmsnorm_rows_that_are_not_numbers():
     """An infinity or NaN stays in its row and shows in its 8-bit block; a row of
     zeros is zeros."""
