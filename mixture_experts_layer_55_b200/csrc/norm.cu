@@ -21,6 +21,28 @@ namespace moe {
 
 constexpr int kNormMaxThreads = 1024;
 
+// These kernels are launched while the one before them in the stream still ends
+// (43.1 us of work took 46.6 in a row of plain launches, 44.6 so) and wait for it
+// here, before they touch memory.
+MOE_DEVICE void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+static cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                                const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Eight elements as they lie in memory, and as fp32.
 template <typename T> struct Row8;
 template <> struct Row8<__nv_bfloat16> {
@@ -126,6 +148,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
     const int64_t team = a.warps == 1 ? (int64_t)blockIdx.x * teams + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = (int64_t)gridDim.x * teams;
     const int tid = a.warps == 1 ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+    wait_for_stream();
     typename R::Raw rx[VPT], rr[VPT];
     auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -284,6 +307,7 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_backward_kernel(const T* dn, con
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    wait_for_stream();
     typename R::Raw rs[VPT], rn[VPT], rd[VPT];
     float r_next = 0.f;
     auto fetch = [&](int64_t row) {
@@ -389,6 +413,7 @@ __global__ void __launch_bounds__(256) rmsnorm_dgamma_kernel(const float* part, 
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int d = (int)blockIdx.x * 32 + lane;
     float t = 0.f;
+    wait_for_stream();
     if (d < D) {
 #pragma unroll 8
         for (int p = w; p < teams; p += 8) t += part[(int64_t)p * D + d];
@@ -440,8 +465,8 @@ static cudaError_t launch_norm_v(int64_t rows, const T* x, const T* residual, T*
         cached[w].store(per_sm, std::memory_order_relaxed);
     }
     const int64_t need = (rows + p.rows_per_block - 1) / p.rows_per_block, most = 148 * (int64_t)per_sm;
-    kernel<<<(unsigned)(need < most ? need : most), p.threads, 0, s>>>(x, residual, s_out, n_out, a);
-    return cudaGetLastError();
+    return launch_early(kernel, (unsigned)(need < most ? need : most), (unsigned)p.threads, 0, s, x, residual, s_out,
+                        n_out, a);
 }
 
 template <typename T>
@@ -515,8 +540,7 @@ static cudaError_t launch_norm_bwd_v(int64_t* blocks, const T* dn, const T* ds, 
         cached[w].store(per_sm, std::memory_order_relaxed);
     }
     if (*blocks > 148 * (int64_t)per_sm) *blocks = 148 * (int64_t)per_sm;
-    kernel<<<(unsigned)*blocks, p.threads, smem, s>>>(dn, ds, s_in, dx, a);
-    return cudaGetLastError();
+    return launch_early(kernel, (unsigned)*blocks, (unsigned)p.threads, smem, s, dn, ds, s_in, dx, a);
 }
 
 template <typename T>
@@ -550,8 +574,8 @@ cudaError_t launch_rmsnorm_backward(int64_t T, int D, int dtype, const void* dn,
     cudaError_t e = dtype == MOE_BF16 ? launch_norm_bwd_t<__nv_bfloat16>(&blocks, dn, ds, s_in, dx, a, p, s)
                                       : launch_norm_bwd_t<float>(&blocks, dn, ds, s_in, dx, a, p, s);
     if (e != cudaSuccess) return e;
-    rmsnorm_dgamma_kernel<<<(D + 31) / 32, 256, 0, s>>>(part, (int)blocks, D, dgamma);
-    return cudaGetLastError();
+    return launch_early(rmsnorm_dgamma_kernel, (unsigned)((D + 31) / 32), 256, 0, s, (const float*)part, (int)blocks, D,
+                        dgamma);
 }
 
 }  // namespace moe
