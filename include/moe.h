@@ -534,7 +534,7 @@ MOE_API moe_status moe_balance_workspace_size(const moe_config *cfg, int64_t S, 
  *   dlogits[t,:] = gradient of c_balance * losses[1] + c_z * losses[0] (the
  *   counts carry none); zero for a token that does not count   (T, E) fp32
  * All are overwritten; dlogits may be NULL.  With no counted token the losses are
- * 0.  Logits of tokens that do not count are not read.  A counted token's NaN
+ * 0.  Logits of tokens that do not count do not matter.  A counted token's NaN
  * shows in its sequence's loss, the losses and its own gradient.  An id outside
  * 0 .. E - 1 raises the bounds flag and is not counted.  Bit-reproducible.
  * logits (T, E) fp32 and topk_ids (T, K) as moe_route writes them; the fields

@@ -352,7 +352,7 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) bal
         // scores.  The fast exponential and reciprocal are good to 2^-22 and the
         // rounding of their argument, |l - max| 2^-24, which the subtraction has too.
         mx = group_max<L>(mx);
-        float se = 0.f, sg = 0.f, one_less[kBalPer];
+        float se = 0.f, sg = 0.f, c = 0.f, one_less[kBalPer];
 #pragma unroll
         for (int j = 0; j < kBalPer; ++j) {
             p[j] = __expf(l[j] - mx);  // 0 for the lanes' places behind E, which hold -inf
@@ -363,21 +363,14 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) bal
                 one_less[j] = 1.f - sc;
                 sg += sc;
             }
-        }
-        se = group_sum<L>(se);
-        const float lse = mx + logf(se), inv_se = __fdividef(1.f, se);
-        if (a.sigmoid) {
-            const float inv_sg = __fdividef(1.f, group_sum<L>(sg));
-#pragma unroll
-            for (int j = 0; j < kBalPer; ++j) l[j] *= inv_sg;
-        }
-        float c = 0.f;
-#pragma unroll
-        for (int j = 0; j < kBalPer; ++j) {
-            p[j] *= inv_se;
             c = fmaf(f[j], a.sigmoid ? l[j] : p[j], c);
         }
+        se = group_sum<L>(se);
         c = group_sum<L>(c);
+        if (a.sigmoid) sg = group_sum<L>(sg);
+        const float lse = mx + logf(se), inv_se = __fdividef(1.f, se);
+        const float inv_sg = a.sigmoid ? __fdividef(1.f, sg) : 0.f;
+        c *= a.sigmoid ? inv_sg : inv_se;
         if (t >= t1) continue;
         if (i >= 0 && lg == 0) {
             z = fma((double)lse, (double)lse, z);
@@ -386,7 +379,7 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) bal
         }
         if (a.dlogits != nullptr) {
             float d[kBalPer];
-            const float cb = cb0 * inv_n, cz = cz0 * lse;
+            const float cb = cb0 * inv_n * (a.sigmoid ? inv_sg : inv_se), cz = cz0 * lse * inv_se;
 #pragma unroll
             for (int j = 0; j < kBalPer; ++j) {
                 const float dp = a.sigmoid ? l[j] * one_less[j] : p[j];
