@@ -404,6 +404,9 @@ MOE_API int32_t moe_backward_kernel_count(const moe_config *cfg);
  * becomes NaN as a whole (byte 255, elements 0x7f).  Data from elsewhere may
  * use any scales.  Rows of n elements are n bytes, their scales n / 32 bytes,
  * both dense and row-major.
+ *
+ * A workspace serves one call at a time: calls that may run at the same time (on
+ * other streams, in graphs replayed together) need one each.
  */
 
 /*

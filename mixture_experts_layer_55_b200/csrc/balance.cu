@@ -27,7 +27,7 @@
 // for 8 experts as for 256.  Bound: latency (launch, two barriers, a handful of
 // dependent loads) up to a few megabytes of logits, then the instructions of a
 // token's softmax.  Measured (softmax, gradient; in us): T = 8192, E = 8, 4
-// sequences 10.2; T = 32768, E = 256, 16 sequences 26.6 (its logits and gradient
+// sequences 10.3; T = 32768, E = 256, 16 sequences 25.2 (its logits and gradient
 // take 10.2 at the measured copy bandwidth).  As three launches, with a warp per
 // token: 30 and 64.
 #include "internal.h"
@@ -64,7 +64,7 @@ struct BalArgs {
     float* seq_loss;
     float* dlogits;
     int64_t T, chunk;  // tokens, tokens per block
-    int E, K, S, sigmoid;
+    int E, K, S;
     float c_balance, c_z;
     BalScratch w;
 };
@@ -191,7 +191,7 @@ MOE_DEVICE void bal_store(float* row, int lg, int E, const float (&v)[kBalPer])
     }
 }
 
-template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) balance_kernel(const BalArgs a)
+template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThreads, 3) balance_kernel(const BalArgs a)
 {
     __shared__ BalShared sh;
     const int tid = threadIdx.x, E = a.E;
@@ -357,20 +357,20 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) bal
         for (int j = 0; j < kBalPer; ++j) {
             p[j] = __expf(l[j] - mx);  // 0 for the lanes' places behind E, which hold -inf
             se += p[j];
-            if (a.sigmoid) {
+            if (SIG) {
                 const float sc = __fdividef(1.f, 1.f + __expf(-l[j]));
                 l[j] = sc;
                 one_less[j] = 1.f - sc;
                 sg += sc;
             }
-            c = fmaf(f[j], a.sigmoid ? l[j] : p[j], c);
+            c = fmaf(f[j], SIG ? l[j] : p[j], c);
         }
         se = group_sum<L>(se);
         c = group_sum<L>(c);
-        if (a.sigmoid) sg = group_sum<L>(sg);
+        if (SIG) sg = group_sum<L>(sg);
         const float lse = mx + logf(se), inv_se = __fdividef(1.f, se);
-        const float inv_sg = a.sigmoid ? __fdividef(1.f, sg) : 0.f;
-        c *= a.sigmoid ? inv_sg : inv_se;
+        const float inv_sg = SIG ? __fdividef(1.f, sg) : 0.f;
+        c *= SIG ? inv_sg : inv_se;
         if (t >= t1) continue;
         if (i >= 0 && lg == 0) {
             z = fma((double)lse, (double)lse, z);
@@ -379,10 +379,10 @@ template <int L, bool VEC> __global__ void __launch_bounds__(kBalThreads, 3) bal
         }
         if (a.dlogits != nullptr) {
             float d[kBalPer];
-            const float cb = cb0 * inv_n * (a.sigmoid ? inv_sg : inv_se), cz = cz0 * lse * inv_se;
+            const float cb = cb0 * inv_n * (SIG ? inv_sg : inv_se), cz = cz0 * lse * inv_se;
 #pragma unroll
             for (int j = 0; j < kBalPer; ++j) {
-                const float dp = a.sigmoid ? l[j] * one_less[j] : p[j];
+                const float dp = SIG ? l[j] * one_less[j] : p[j];
                 d[j] = i >= 0 ? cb * dp * (f[j] - c) + cz * p[j] : 0.f;
             }
             bal_store<L, VEC>(a.dlogits + t * E, lg, E, d);
@@ -465,7 +465,7 @@ static BalLayout balance_layout(int64_t S)
 }
 size_t balance_bytes(const moe_config&, int64_t S) { return balance_layout(S).total; }
 
-template <int L, bool VEC> static cudaError_t launch_balance_t(BalArgs a, cudaStream_t s)
+template <int L, bool VEC, bool SIG> static cudaError_t launch_balance_t(BalArgs a, cudaStream_t s)
 {
     // resident blocks, per device (the launch is cooperative)
     static std::atomic<int> cached[32];
@@ -475,7 +475,7 @@ template <int L, bool VEC> static cudaError_t launch_balance_t(BalArgs a, cudaSt
     int resident = dev >= 0 && dev < 32 ? cached[dev].load(std::memory_order_acquire) : 0;
     if (resident == 0) {
         int per_sm = 0, sms = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, balance_kernel<L, VEC>, kBalThreads, 0);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, balance_kernel<L, VEC, SIG>, kBalThreads, 0);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
         resident = per_sm * sms;
@@ -488,13 +488,14 @@ template <int L, bool VEC> static cudaError_t launch_balance_t(BalArgs a, cudaSt
     a.chunk = (a.T + blocks - 1) / blocks;
     blocks = (a.T + a.chunk - 1) / a.chunk;  // none without tokens
     void* args[] = {&a};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(balance_kernel<L, VEC>), dim3((unsigned)blocks),
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(balance_kernel<L, VEC, SIG>), dim3((unsigned)blocks),
                                        dim3(kBalThreads), args, 0, s);
 }
 
-template <int L> static cudaError_t launch_balance_l(const BalArgs& a, cudaStream_t s)
+template <int L> static cudaError_t launch_balance_l(const BalArgs& a, bool sigmoid, cudaStream_t s)
 {
-    return a.E % 4 == 0 ? launch_balance_t<L, true>(a, s) : launch_balance_t<L, false>(a, s);
+    if (sigmoid) return a.E % 4 == 0 ? launch_balance_t<L, true, true>(a, s) : launch_balance_t<L, false, true>(a, s);
+    return a.E % 4 == 0 ? launch_balance_t<L, true, false>(a, s) : launch_balance_t<L, false, false>(a, s);
 }
 
 cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, const int32_t* ids,
@@ -506,7 +507,8 @@ cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, 
     BalArgs a;
     a.logits = logits; a.ids = ids; a.starts = starts; a.mask = mask;
     a.counts = counts; a.losses = losses; a.seq_loss = seq_loss; a.dlogits = dlogits;
-    a.T = c.T; a.chunk = 0; a.E = c.E; a.K = c.K; a.S = (int)S; a.sigmoid = c.score_func == MOE_SCORE_SIGMOID;
+    a.T = c.T; a.chunk = 0; a.E = c.E; a.K = c.K; a.S = (int)S;
+    const bool sigmoid = c.score_func == MOE_SCORE_SIGMOID;
     a.c_balance = c_balance; a.c_z = c_z;
     a.w.status = reinterpret_cast<int*>(w + L.head);
     a.w.bar = reinterpret_cast<uint32_t*>(w + L.head + 64);
@@ -515,12 +517,12 @@ cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, 
     a.w.bad = reinterpret_cast<int*>(w + L.bad);
     a.w.acc = reinterpret_cast<unsigned long long*>(w + L.acc);
     a.w.zpart = reinterpret_cast<double*>(w + L.zpart);
-    if (c.E <= 8) return launch_balance_l<1>(a, s);
-    if (c.E <= 16) return launch_balance_l<2>(a, s);
-    if (c.E <= 32) return launch_balance_l<4>(a, s);
-    if (c.E <= 64) return launch_balance_l<8>(a, s);
-    if (c.E <= 128) return launch_balance_l<16>(a, s);
-    return launch_balance_l<32>(a, s);
+    if (c.E <= 8) return launch_balance_l<1>(a, sigmoid, s);
+    if (c.E <= 16) return launch_balance_l<2>(a, sigmoid, s);
+    if (c.E <= 32) return launch_balance_l<4>(a, sigmoid, s);
+    if (c.E <= 64) return launch_balance_l<8>(a, sigmoid, s);
+    if (c.E <= 128) return launch_balance_l<16>(a, sigmoid, s);
+    return launch_balance_l<32>(a, sigmoid, s);
 }
 
 }  // namespace moe
