@@ -46,15 +46,17 @@ static moe_status check_mx8_weights(const moe_mx8_weights* w)
     return MOE_OK;
 }
 
-// the status region, then the experts' A maps
+// the status region, the experts' A maps, the parts of a cut down product
+static size_t mx8_maps_at() { return align_up(64 * sizeof(int)); }
+static size_t mx8_part_at(const moe_config& c) { return mx8_maps_at() + align_up(2 * (size_t)c.E * kTensorMapBytes); }
 static size_t mx8_ws_bytes(const moe_config& c)
 {
-    return align_up(64 * sizeof(int)) + align_up(2 * (size_t)c.E * kTensorMapBytes);
+    return mx8_part_at(c) + align_up(mx8_part_bytes(c, max_rows_of(c)));
 }
 
 struct FwdMx8Layout {
     WsLayout ws;
-    size_t amaps, ids, w, counts, kept, offsets, perm, row_of;
+    size_t amaps, part, ids, w, counts, kept, offsets, perm, row_of;
     size_t xq, xs, xq_perm, xs_perm, hq, hs, y_perm, total;
 };
 static FwdMx8Layout fwd_mx8_layout(const moe_config& c)
@@ -64,6 +66,7 @@ static FwdMx8Layout fwd_mx8_layout(const moe_config& c)
     const size_t tk = (size_t)c.T * c.K, R = (size_t)max_rows_of(c);
     size_t o = F.ws.total;
     F.amaps = o;   o += align_up(2 * (size_t)c.E * kTensorMapBytes);
+    F.part = o;    o += align_up(mx8_part_bytes(c, max_rows_of(c)));
     F.ids = o;     o += align_up(tk * sizeof(int32_t));
     F.w = o;       o += align_up(tk * sizeof(float));
     F.counts = o;  o += align_up((size_t)c.E * sizeof(int32_t));
@@ -196,8 +199,9 @@ moe_status moe_expert_ffn_mx8(const moe_config* cfg, const void* xq, const void*
     st = check_scratch(workspace, workspace_bytes, mx8_ws_bytes(*cfg));
     if (st != MOE_OK) return st;
     return cuda_status(launch_ffn_mx8(*cfg, max_rows_of(*cfg), xq, xs, offsets, perm, topk_w, *weights, hq, hs,
-                                      y_perm, static_cast<char*>(workspace) + align_up(64 * sizeof(int)),
-                                      static_cast<int*>(workspace), static_cast<cudaStream_t>(stream)));
+                                      y_perm, static_cast<char*>(workspace) + mx8_maps_at(),
+                                      static_cast<char*>(workspace) + mx8_part_at(*cfg), static_cast<int*>(workspace),
+                                      static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_forward_mx8_workspace_size(const moe_config* cfg, size_t* bytes)
@@ -253,7 +257,7 @@ moe_status moe_forward_mx8(const moe_config* cfg, const void* x, const void* xq,
         e = launch_mx8_gather(c, xq, xs, offsets, perm, ws + F.xq_perm, ws + F.xs_perm, max_rows, status, s);
     if (e == cudaSuccess)
         e = launch_ffn_mx8(c, max_rows, ws + F.xq_perm, ws + F.xs_perm, offsets, perm, w, *weights, ws + F.hq,
-                           ws + F.hs, ws + F.y_perm, ws + F.amaps, status, s);
+                           ws + F.hs, ws + F.y_perm, ws + F.amaps, ws + F.part, status, s);
     if (e == cudaSuccess) e = launch_combine(c, ws + F.y_perm, row_of, nullptr, y_add, y, max_rows, s);
     return cuda_status(e);
 }

@@ -118,6 +118,8 @@ struct Args {
     int64_t max_rows, nk;
     int* status;
     const CUtensorMap* amaps;  // A's map per expert (null: tmA)
+    int splits;                // few rows, down: the contracted axis is cut in this many parts
+    float* part;               // their sums (splits, max_rows, N) where splits > 1
 };
 
 // ------------------------------------------------------------------- PTX --
@@ -769,7 +771,7 @@ template <> MOE_DEVICE void tmem_ld<8>(uint32_t taddr, uint32_t (&r)[8])
                  : "r"(taddr));
 }
 
-template <bool GATEUP, int NT>
+template <bool GATEUP, int NT, bool CUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     ffn_mx8_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
                        const __grid_constant__ CUtensorMap tmW1, const Args a)
@@ -812,8 +814,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = m->tmem_base;
-    const int total = m->pref[E];
-    const int num_kb = (a.Kdim + BK - 1) / BK;
+    const int splits = CUT ? a.splits : 1;
+    const int total = m->pref[E] * splits;  // work items: (tile, part of the contracted axis)
+    const int num_kb = (a.Kdim + BK - 1) / BK, groups = (num_kb + 3) / 4;
+    // an item's stages are whole groups of four, so that its scales' loads stay aligned
+    auto first_group = [&](int sp) { return groups * sp / splits; };
+    auto end_kb = [&](int sp) { return sp == splits - 1 ? num_kb : 4 * first_group(sp + 1); };
     volatile int* abort_flag = &m->abort_flag;
     // the down product starts under the gate/up product's end, as above
     if (GATEUP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -842,16 +848,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (!GATEUP) {
                 if (unit < total) {
                     int e, m_row0, row_end, n0;
-                    decode_tile(m, E, NT, BN, unit, e, m_row0, row_end, n0);
-                    early = num_kb < STAGES ? num_kb : STAGES;
-                    for (int kb = 0; kb < early; ++kb) weights(kb, kb, e, n0);
+                    decode_tile(m, E, NT, BN, unit / splits, e, m_row0, row_end, n0);
+                    const int kb0 = 4 * first_group(unit % splits), n = end_kb(unit % splits) - kb0;
+                    early = n < STAGES ? n : STAGES;
+                    for (int st = 0; st < early; ++st) weights(st, kb0 + st, e, n0);
                 }
                 asm volatile("griddepcontrol.wait;" ::: "memory");
             }
             for (int t = unit; t < total && ok; t += units) {
                 int e, m_row0, row_end, n0;
-                decode_tile(m, E, NT, BN, t, e, m_row0, row_end, n0);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                decode_tile(m, E, NT, BN, t / splits, e, m_row0, row_end, n0);
+                const int kb1 = end_kb(t % splits);
+                for (int kb = 4 * first_group(t % splits); kb < kb1; ++kb) {
                     if (!mbar_wait(&m->empty[stage], phase ^ 1u, a.status, 742, abort_flag)) {
                         ok = false;
                         break;
@@ -895,7 +903,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (!warp_wait_all(&m->tempty[acc], acc_phase ^ 1u, a.status, 744, abort_flag)) break;
             tc_fence_after();
             const uint32_t d0 = tbase + (uint32_t)(acc * 2 * NT);
-            for (int kb = 0; kb < num_kb; ++kb) {
+            const int kb0 = 4 * first_group(t % splits), kb1 = end_kb(t % splits);
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if ((in_slot == 0 && !warp_wait_all(&m->sfull[slot], sphase, a.status, 747, abort_flag)) ||
                     !warp_wait_all(&m->full[stage], phase, a.status, 746, abort_flag)) {
                     ok = false;
@@ -915,13 +924,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int kk = 0; kk < BK / 32; ++kk)
                         mma_mx8<false>(leader, d0 + b * NT, wdesc + (b * G::W_BYTES >> 4) + kk * 2, xdesc + kk * 2,
                                        idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), tsf + 4 + 4 * b, tsf,
-                                       kk != 0 ? 1u : (kb != 0 ? 1u : 0u));
+                                       kk != 0 ? 1u : (kb != kb0 ? 1u : 0u));
                 commit<false>(leader, s_empty + (uint32_t)stage * 8);
                 if (++stage == STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
-                if (++in_slot == SF_GROUP || kb == num_kb - 1) {
+                if (++in_slot == SF_GROUP || kb == kb1 - 1) {
                     commit<false>(leader, s_sempty + (uint32_t)slot * 8);
                     in_slot = 0;
                     if (++slot == SF_SLOTS) {
@@ -944,12 +953,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else if (warp < EPI_WARP0) {
         // ------------------------------------------------ scales
         const int i = (warp - 2) * 32 + lane;
-        const int nb = a.Kdim / kMxBlock, groups = (num_kb + 3) / 4;
+        const int nb = a.Kdim / kMxBlock;
         const uint32_t off = (uint32_t)((i & 31) * 16 + (i >> 5) * 4);
         const uint8_t *px = nullptr, *pw0 = nullptr, *pw1 = nullptr;
         auto rows_of = [&](int t) {
             int e, m_row0, row_end, n0;
-            decode_tile(m, E, NT, BN, t, e, m_row0, row_end, n0);
+            decode_tile(m, E, NT, BN, t / splits, e, m_row0, row_end, n0);
             const int64_t row = (int64_t)m_row0 + i;
             px = i < NT && row < row_end ? a.as + row * nb : nullptr;
             const int n = n0 + i, n2 = GATEUP ? n : n + 128;
@@ -958,7 +967,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             pw1 = n2 < a.N ? (GATEUP ? a.b1s : a.b0s) + (be + n2) * nb : nullptr;
         };
         uint4 vx[2], v0[2], v1[2];
-        int ld_t = unit, ld_g = 0;
+        int ld_t = unit, ld_g = unit < total ? first_group(unit % splits) : 0;
+        bool fresh = true;
         auto load_weights = [&](int i2) {
             v0[i2] = load_scales(pw0, ld_g, nb);
             v1[i2] = load_scales(pw1, ld_g, nb);
@@ -966,20 +976,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         auto load_tokens = [&](int i2) { vx[i2] = load_scales(px, ld_g, nb); };
         auto load_next = [&](int i2) {
             if (ld_t >= total) return;
-            if (ld_g == 0) rows_of(ld_t);
+            if (fresh) rows_of(ld_t);
             load_weights(i2);
             load_tokens(i2);
-            if (++ld_g == groups) {
-                ld_g = 0;
+            fresh = 4 * ++ld_g >= end_kb(ld_t % splits);
+            if (fresh) {
                 ld_t += units;
+                ld_g = first_group(ld_t % splits);
             }
         };
         if (!GATEUP) asm volatile("griddepcontrol.wait;" ::: "memory");
         load_next(0);
         load_next(1);
-        int slot = 0, kb_left = num_kb;
+        int slot = 0;
         uint32_t sphase = 0;
-        const int64_t mine = unit < total ? (int64_t)((total - unit + units - 1) / units) * groups : 0;
+        int64_t mine = 0;  // this CTA's groups
+        for (int t = unit; t < total; t += units)
+            mine += (end_kb(t % splits) + 3) / 4 - first_group(t % splits);
         for (int64_t n = 0; n < mine; n += 2) {
             bool ok = true;
 #pragma unroll
@@ -1003,8 +1016,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     slot = 0;
                     sphase ^= 1u;
                 }
-                kb_left -= SF_GROUP;
-                if (kb_left <= 0) kb_left = num_kb;
                 load_next(i2);
             }
             if (!ok) break;
@@ -1017,10 +1028,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t acc_phase = 0;
         for (int t = unit; t < total; t += units) {
             int e, m_row0, row_end, n0;
-            decode_tile(m, E, NT, BN, t, e, m_row0, row_end, n0);
+            decode_tile(m, E, NT, BN, t / splits, e, m_row0, row_end, n0);
             const int rows = row_end - m_row0 < NT ? row_end - m_row0 : NT;
             float w = 1.f;  // lane j: token j's weight
-            if (!GATEUP && a.perm != nullptr && lane < rows) {
+            if (!GATEUP && !CUT && a.perm != nullptr && lane < rows) {
                 const int32_t pa = a.perm[m_row0 + lane];
                 w = 0.f;
                 if (pa >= 0 && (int64_t)pa < a.nk) w = a.topk_w[pa];
@@ -1057,6 +1068,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         if (j >= rows) break;
+                        if (CUT) {
+                            a.part[((int64_t)(t % splits) * a.max_rows + m_row0 + j) * a.N + d0 + lane] =
+                                __uint_as_float(v[j]);
+                            continue;
+                        }
                         const float wj = __shfl_sync(0xffffffffu, w, j);
                         a.y[((int64_t)m_row0 + j) * a.N + d0 + lane] = __float2bfloat16_rn(wj * __uint_as_float(v[j]));
                     }
@@ -1078,6 +1094,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem_base, G::TMEM);
     }
+}
+
+// y = bf16(w (part 0 + part 1 + ...)), in that order: the rows of a down product whose
+// contracted axis was cut.  A thread per 4 elements.
+__global__ void __launch_bounds__(256) ffn_mx8_join_kernel(const Args a)
+{
+    bool bad = false;
+    for (int e = threadIdx.x; e < a.E; e += 256) {
+        const int r0 = a.offsets[e], r1 = a.offsets[e + 1];
+        bad |= r0 < 0 || r1 < r0 || (int64_t)r1 > a.max_rows;
+    }
+    if (__syncthreads_or(bad)) return;  // nothing was computed (the products raised the flag)
+    const int64_t row = blockIdx.y;
+    if (row < a.offsets[0] || row >= a.offsets[a.E]) return;
+    float w = 1.f;
+    if (a.perm != nullptr) {
+        const int32_t pa = a.perm[row];
+        w = 0.f;
+        if (pa >= 0 && (int64_t)pa < a.nk) w = a.topk_w[pa];
+        else if (blockIdx.x == 0 && threadIdx.x == 0) raise_flag(a.status, kFlagBounds, 751);
+    }
+    const int d = 4 * (int)(blockIdx.x * 256 + threadIdx.x);
+    if (d >= a.N) return;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int sp = 0; sp < a.splits; ++sp) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part + ((int64_t)sp * a.max_rows + row) * a.N + d);
+        t.x += v.x;
+        t.y += v.y;
+        t.z += v.z;
+        t.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(a.y + row * a.N + d) = make_uint2(pack_bf16x2(w * t.x, w * t.y), pack_bf16x2(w * t.z, w * t.w));
 }
 
 // ------------------------------------------------------------------- host --
@@ -1205,13 +1253,13 @@ static cudaError_t launch_one(const CUtensorMap& mA, const CUtensorMap& mB0, con
     return cudaLaunchKernelEx(&cfg, ffn_mx8_kernel<GATEUP, PAIR>, mA, mB0, mB1, mY, a);
 }
 
-template <bool GATEUP, int NT>
+template <bool GATEUP, int NT, bool CUT>
 static cudaError_t launch_few(const CUtensorMap& mX, const CUtensorMap& mW0, const CUtensorMap& mW1, const Args& a,
                               int64_t tiles_bound, cudaStream_t s)
 {
     static PerDeviceFlag opted;
     int dev = 0, sms = 0;
-    cudaError_t e = opt_in_smem(opted, reinterpret_cast<const void*>(ffn_mx8_few_kernel<GATEUP, NT>), Few<NT>::SMEM);
+    cudaError_t e = opt_in_smem(opted, reinterpret_cast<const void*>(ffn_mx8_few_kernel<GATEUP, NT, CUT>), Few<NT>::SMEM);
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -1225,15 +1273,42 @@ static cudaError_t launch_few(const CUtensorMap& mX, const CUtensorMap& mW0, con
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = GATEUP ? 0 : 1;
-    return cudaLaunchKernelEx(&cfg, ffn_mx8_few_kernel<GATEUP, NT>, mX, mW0, mW1, a);
+    return cudaLaunchKernelEx(&cfg, ffn_mx8_few_kernel<GATEUP, NT, CUT>, mX, mW0, mW1, a);
 }
 
 }  // namespace mx
 
+// Tiles of few rows there can be, for n_tiles tiles along the product's columns.
+static int64_t few_tiles(const moe_config& c, int64_t max_rows, int n_tiles)
+{
+    const int64_t m = c.E + max_rows / 32;
+    return (max_rows < m ? max_rows : m) * n_tiles;
+}
+
+// Parts the down product's contracted axis is cut in: with few tokens its tiles leave
+// most SMs without a stream of weights.  (One token, 2 of 8 experts, D = 4096,
+// F = 14336: both products 90 us with 32 tiles for 148 SMs, 70 with each in four
+// parts and a kernel that joins them.)
+static int few_splits(const moe_config& c, int64_t max_rows)
+{
+    if (max_rows > mx::kFewRows * (int64_t)c.E) return 1;
+    const int64_t tiles = few_tiles(c, max_rows, (c.D + 255) / 256), groups = (c.F + 511) / 512;
+    int64_t n = 148 / tiles;
+    if (n > 8) n = 8;
+    if (n > groups / 2) n = groups / 2;  // two groups of four stages each at least
+    return n > 1 ? (int)n : 1;
+}
+
+size_t mx8_part_bytes(const moe_config& c, int64_t max_rows)
+{
+    const int n = few_splits(c, max_rows);
+    return n > 1 ? (size_t)n * (size_t)max_rows * c.D * sizeof(float) : 0;
+}
+
 cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq, const void* xs,
                            const int32_t* offsets, const int32_t* perm, const float* topk_w,
-                           const moe_mx8_weights& w, void* hq, void* hs, void* y_perm, void* amaps, int* status,
-                           cudaStream_t s)
+                           const moe_mx8_weights& w, void* hq, void* hs, void* y_perm, void* amaps, void* part,
+                           int* status, cudaStream_t s)
 {
     using namespace mx;
     auto u8 = [](const void* p) { return static_cast<const uint8_t*>(p); };
@@ -1255,9 +1330,17 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
             !map_bytes(&mU, w.up, D, F, E, 128) || !map_bytes(&mH, hq, F, R, 0, NT) ||
             !map_bytes(&mD, w.down, F, D, E, 128))
             return cudaErrorInvalidValue;
-        const int64_t mt = max_rows < c.E ? max_rows : (max_rows + NT - 1) / NT + c.E;
-        cudaError_t e = launch_few<true, NT>(mX, mG, mU, a, mt * a.n_tiles, s);
-        return e != cudaSuccess ? e : launch_few<false, NT>(mH, mD, mD, d, mt * d.n_tiles, s);
+        a.splits = 1;
+        d.splits = few_splits(c, max_rows);
+        d.part = static_cast<float*>(part);
+        cudaError_t e = launch_few<true, NT, false>(mX, mG, mU, a, few_tiles(c, max_rows, a.n_tiles), s);
+        if (e != cudaSuccess) return e;
+        const int64_t tiles = few_tiles(c, max_rows, d.n_tiles);
+        if (d.splits == 1) return launch_few<false, NT, false>(mH, mD, mD, d, tiles, s);
+        e = launch_few<false, NT, true>(mH, mD, mD, d, tiles * d.splits, s);
+        if (e != cudaSuccess) return e;
+        ffn_mx8_join_kernel<<<dim3((unsigned)((c.D + 1023) / 1024), (unsigned)max_rows), 256, 0, s>>>(d);
+        return cudaGetLastError();
     }
     if (!map_bytes(&mX, xq, D, R, 0, 128) || !map_bytes(&mG, w.gate, D, F, E, 64) ||
         !map_bytes(&mU, w.up, D, F, E, 64) || !map_bytes(&mH, hq, F, R, 0, 128) ||

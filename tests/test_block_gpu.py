@@ -558,7 +558,10 @@ EXPERTS = [(1, 32, 32, 1, 1, None), (1, 256, 512, 8, 2, None), (3, 96, 160, 2, 2
            (4, 7168, 64, 256, 8, None), (2000, 2048, 256, 8, 2, None), (60, 224, 160, 8, 2, [70, 0, 33, 1, 16, 0, 0, 0]),
            (20, 1408, 2080, 4, 2, None), (96, 32, 544, 8, 2, [0, 32, 32, 64, 31, 33, 0, 0]),
            # several tiles a CTA in each form (pairs, single CTAs, few rows)
-           (1500, 256, 2816, 8, 2, None), (200, 128, 4096, 8, 2, None), (150, 4096, 1536, 24, 3, None)]
+           (1500, 256, 2816, 8, 2, None), (200, 128, 4096, 8, 2, None), (150, 4096, 1536, 24, 3, None),
+           # few tokens: the down product's contracted axis in parts (4, 5, 2, 8)
+           (1, 256, 4096, 8, 2, None), (3, 224, 5600, 4, 2, None), (20, 512, 2080, 1, 1, None),
+           (60, 96, 8192, 4, 1, [40, 0, 20, 0])]
 
 
 @pytest.mark.parametrize("case", range(len(EXPERTS)))
@@ -572,25 +575,27 @@ def test_experts_mx8(case):
     assert torch.equal(y, y2) and torch.equal(hq, hq2) and torch.equal(hs, hs2)
 
 
-@pytest.mark.parametrize("T,E,counts", [(100, 3, [70, 0, 50]), (40, 6, [0, 33, 1, 0, 6, 0]), (400, 3, [300, 0, 129])])
-def test_experts_mx8_unit_weights_and_unused_rows(T, E, counts):
+@pytest.mark.parametrize("T,E,F,counts", [(100, 3, 96, [70, 0, 50]), (40, 6, 96, [0, 33, 1, 0, 6, 0]),
+                                          (400, 3, 96, [300, 0, 129]), (10, 3, 2048, [5, 0, 9])])
+def test_experts_mx8_unit_weights_and_unused_rows(T, E, F, counts):
     """Weight 1 without perm; rows behind offsets[E] stay as they were."""
-    st = _experts_state(T, 128, 96, E, 2, 9, counts=counts)  # fewer than the 2 T rows there are
+    st = _experts_state(T, 128, F, E, 2, 9, counts=counts)  # fewer than the 2 T rows there are
     used = sum(counts)
     hq, hs, y, ws = _run_experts(st, weighted=False)
     assert B.moe_get_device_status(ws) == 0
     _check_experts(st, hq, hs, y, weighted=False)
     assert bool((y[used:] == 7).all()) and bool((hq[used:] == 0x55).all()) and bool((hs[used:] == 0x55).all())
-    none = _experts_state(T, 64, 64, E, 2, 9, counts=[0] * E)
+    none = _experts_state(T, 64, F, E, 2, 9, counts=[0] * E)
     hq, hs, y, ws = _run_experts(none)
     assert B.moe_get_device_status(ws) == 0 and bool((y == 7).all()) and bool((hq == 0x55).all())
 
 
-@pytest.mark.parametrize("T,E", [(50, 2), (50, 8), (300, 2)])  # single CTAs, few rows, CTA pairs
-def test_experts_mx8_faults_are_seen(T, E):
+# single CTAs, few rows, CTA pairs, few rows with the down product in parts
+@pytest.mark.parametrize("T,E,F", [(50, 2, 128), (50, 8, 128), (300, 2, 128), (20, 8, 4096)])
+def test_experts_mx8_faults_are_seen(T, E, F):
     """A NaN scale makes its row NaN and no other; malformed offsets compute nothing
     and raise the bounds flag, as does a perm entry out of range."""
-    st = _experts_state(T, 256, 128, E, 1, 4)
+    st = _experts_state(T, 256, F, E, 1, 4)
     _, _, y0, _ = _run_experts(st)
     st["xs"] = st["xs"].clone()
     st["xs"][17, 3] = 255
@@ -598,7 +603,7 @@ def test_experts_mx8_faults_are_seen(T, E):
     assert bool(y[17].isnan().all()) and bool((hs[17] == 255).all())
     keep = [r for r in range(T) if r != 17]
     assert torch.equal(y[keep], y0[keep])
-    st = _experts_state(T, 256, 128, E, 1, 4)
+    st = _experts_state(T, 256, F, E, 1, 4)
     good = st["offsets"].tolist()
     for bad in (good[:-1] + [T + 1], good[:1] + [T - 1] + good[1:-1], [-5] + good[1:]):
         st2 = dict(st, offsets=torch.tensor(bad, dtype=torch.int32, device="cuda"))
@@ -615,9 +620,9 @@ def test_experts_mx8_faults_are_seen(T, E):
     assert B.moe_get_device_status(ws) == 0 and torch.equal(y, y0)
 
 
-@pytest.mark.parametrize("T,E", [(200, 4), (30, 8), (400, 2)])
-def test_experts_mx8_on_another_stream_and_in_a_graph(T, E):
-    st = _experts_state(T, 256, 192, E, 2, 21)
+@pytest.mark.parametrize("T,E,F", [(200, 4, 192), (30, 8, 192), (400, 2, 192), (2, 8, 4096)])
+def test_experts_mx8_on_another_stream_and_in_a_graph(T, E, F):
+    st = _experts_state(T, 256, F, E, 2, 21)
     hq, hs, y0, _ = _run_experts(st)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
