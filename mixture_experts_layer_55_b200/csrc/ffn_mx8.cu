@@ -1295,7 +1295,9 @@ static int few_splits(const moe_config& c, int64_t max_rows)
     const int64_t tiles = few_tiles(c, max_rows, (c.D + 255) / 256), groups = (c.F + 511) / 512;
     int64_t n = 148 / tiles;
     if (n > 8) n = 8;
-    if (n > groups / 2) n = groups / 2;  // two groups of four stages each at least
+    // two groups of four stages each at least (D = 2048, F = 1408, 6 of 64 experts: 22.5 us
+    // whole, 23.6 in three parts of one group)
+    if (n > groups / 2) n = groups / 2;
     return n > 1 ? (int)n : 1;
 }
 
