@@ -421,9 +421,10 @@ MOE_API int32_t moe_backward_kernel_count(const moe_config *cfg);
  * otherwise), n (T, D), rstd (T) fp32, q (T, D bytes) with q_scales
  * (T, D / 32 bytes; both or neither, D a multiple of 32: MOE_ERR_ALIGN
  * otherwise).  n or q is required.  Squares are summed in fp32, in other units
- * where they would leave its range.  s and n may be
- * the memory of x or of residual (not each other's).  D <= 65536
- * (MOE_ERR_UNSUPPORTED), T < 2^31.  A row that holds an infinity or NaN gives
+ * where they would leave its range: rows from fp32's least value to its largest
+ * have the norm of the formula, with any eps (rstd alone is an infinity where it
+ * is above fp32's range).  s and n may be the memory of x or of residual (not
+ * each other's).  D <= 65536 (MOE_ERR_UNSUPPORTED), T < 2^31.  A row that holds an infinity or NaN gives
  * what the formulas give; no other row is touched by it.
  */
 MOE_API moe_status moe_rmsnorm(int64_t T, int32_t D, int32_t dtype, const void *x, const void *residual,

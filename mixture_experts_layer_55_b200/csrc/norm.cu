@@ -198,24 +198,24 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
             }
         }
         if (AHEAD && row + step < a.T) fetch(row + step);
-        // rstd as the sum of two fp32 values: fp32's root, and its Newton correction
-        // from the residual 1 - mean r^2, exact but for the last of its roundings.  n
-        // is then the formula's to 2^-24, and what is rounded further, to bf16 and to 8
-        // bits, falls on the formula's side of a border.
         double sum = row_add_wide(ss, red[flip], a.warps);
-        float eps = a.eps, unit = 1.f;
-        if (!(sum < 0x1p100) || (sum < 0x1p-90 && eps < 0x1p-100f)) {
-            // the squares leave fp32 (or the row holds a NaN): again in units of 2^70 or
-            // 2^-70, the whole team together
-            unit = sum < 1.0 ? 0x1p70f : 0x1p-70f;
-            eps *= unit * unit;
+        double eps = a.eps;
+        float half = 1.f;
+        if (!(sum < 0x1p100) || (sum < 0x1p-90 && a.eps < 0x1p-100f)) {
+            // the squares leave fp32 (or the row holds a NaN): again in units of 2^100 or
+            // 2^-70, the whole team together.  The values and the root keep one half of the
+            // unit each, so that both are normal numbers from fp32's least value to its
+            // largest; eps in these units, up to 2^100, is formed in fp64.
+            half = sum < 1.0 ? 0x1p50f : 0x1p-35f;
+            eps *= ((double)half * half) * ((double)half * half);
             float again = 0.f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
                 if (tid + i * tpr < a.nvec)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float u = v[i][j] * unit;
+                        v[i][j] *= half;
+                        const float u = v[i][j] * half;
                         again = fmaf(u, u, again);
                     }
             if (a.warps > 1) __syncthreads();  // the first sum's slots have been read
@@ -225,14 +225,14 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const T* x, const T* resi
         // fp64: n is then the formula's rounded to fp32 but for a percent of cases, and
         // what is rounded further, to bf16 and to 8 bits, falls on the formula's side
         // of a border (the step in fp32 took the same time and missed a third).
-        const double mean = sum * a.inv_d + (double)eps;
+        const double mean = sum * a.inv_d + eps;
         const float root = rsqrtf((float)mean);
         const double fine = (double)root * (1.5 - 0.5 * mean * (double)root * (double)root);
         // (not where the root says it all: a row of zeros without eps, an overflow, a
         // NaN; nor where r0's parts leave fp32)
         const bool carry = gamma_fits && root > 0x1p-60f && root < 0x1p60f;
         const float near = carry ? (float)fine : root;
-        const float r0 = near * unit, r_lo = carry ? (float)(fine - (double)near) * unit : 0.f, r = r0;
+        const float r0 = near * half, r_lo = carry ? (float)(fine - (double)near) * half : 0.f, r = r0 * half;
         if (tid == 0 && a.rstd != nullptr) a.rstd[row] = r;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {

@@ -1,0 +1,77 @@
+"""Edges of the operators around the layer on the GPU: values at the ends of the
+types' ranges, calls that other tests do not make.
+
+A comparison holds where the error is at most a finite tolerance, or where both
+sides are the same infinity: a NaN is off.  Tolerances as in test_block_gpu: a
+rounding is off by at most half a step (bf16 2^-8, fp32 2^-24 of the value), a
+row's sum by 2^-17.
+"""
+import pytest
+import torch
+
+import mixture_experts_layer_55_b200 as M
+from mixture_experts_layer_55_b200 import _binding as B
+
+pytestmark = pytest.mark.gpu
+
+ROUND = {torch.bfloat16: 2.0**-8, torch.float32: 2.0**-24}
+SUM = 2.0**-17
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape, dtype=torch.float32):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def within(got, ref, tol, what=""):
+    got, ref = got.double(), ref.double()
+    tol = torch.as_tensor(tol, dtype=torch.float64, device=got.device).broadcast_to(got.shape)
+    err = (got - ref).abs()
+    ok = ((err <= tol) & tol.isfinite()) | (got == ref)
+    assert bool(ok.all()), (f"{what}: {int((~ok).sum())} off, {int(got.isnan().sum())} NaN, worst "
+                            f"{float((err - tol).nan_to_num(nan=float('inf')).max()):.3e} over the tolerance")
+
+
+# ---------------------------------------------------------------------- norm --
+
+# (rms of the rows, eps): squares below fp32's range with eps 0 and with eps of their
+# own size, above it, at and below the least normal value, at the largest
+RANGE = [(1e-18, 0.0), (1e-18, 1e-36), (1e-18, 1e-31), (1e-20, 7e-31), (1e-30, 0.0), (1e-16, 1e-40), (3e-39, 0.0),
+         (1e-42, 0.0), (1e-42, 1e-44), (1e-12, 0.0), (1e19, 0.0), (1e30, 1e-6), (1.5e38, 0.0), (1.5e38, 1e30), (0.0, 1e-36)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(3, 64), (40, 512), (700, 4096), (2, 16640)])
+@pytest.mark.parametrize("scale,eps", RANGE)
+def test_rmsnorm_range(scale, eps, T, D, dt):
+    """A row of finite values has a finite norm, whatever its size: every row of the
+    range beside rows of ordinary size, which it does not touch."""
+    dtype = DT[dt]
+    if dt == "bf16" and scale > 0:
+        scale = max(scale, 1e-39)  # bf16's least value is 2^-133
+    g = _gen(T + D)
+    x = (0.25 + torch.rand(T, D, generator=g, device="cuda"))
+    x[:, ::3] *= -1
+    x[::2] *= scale
+    x = x.to(dtype)
+    gamma = 1 + 0.3 * _randn(g, D)
+    eps = float(torch.tensor(eps))  # as the call takes it, in fp32
+    n, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+    q, qs = torch.empty(T, D, dtype=torch.uint8, device="cuda"), torch.empty(T, D // 32, dtype=torch.uint8, device="cuda")
+    M.moe_rmsnorm(x, gamma, n, rstd=rstd, q=q, q_scales=qs, eps=eps)
+    r = (x.double().square().mean(1) + eps).rsqrt()
+    # rstd leaves fp32 above (an infinity), or falls below its normal values (a step of 2^-149)
+    big = r > torch.finfo(torch.float32).max
+    assert bool((rstd[big] == float("inf")).all())
+    within(rstd[~big], r[~big], SUM * r[~big] + 2.0**-149, "rstd")
+    ref = x.double() * r[:, None] * gamma.double()
+    within(n, ref, (ROUND[dtype] + SUM) * ref.abs() + 1e-38, "n")
+    assert bool((qs != 255).all())
+    # the 8-bit rows: half an e4m3 step, 2^-4 of a value or half the least step of its block
+    v = q.view(torch.float8_e4m3fn).double().unflatten(-1, (-1, 32)) * torch.exp2(qs.double() - 127)[..., None]
+    step = torch.exp2(qs.double() - 127).repeat_interleave(32, 1)
+    within(v.flatten(-2), n, 2.0**-4 * n.double().abs() + 2.0**-10 * step, "values")
