@@ -348,19 +348,23 @@ template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThrea
 #pragma unroll
             for (int j = 0; j < kBalPer; ++j) f[j] = (float)n[j] * fscale;
         }
-        // softmax: p = exp(l - max) / sum; sigmoid scores: l becomes score / sum of
-        // scores.  The fast exponential and reciprocal are good to 2^-22 and the
-        // rounding of their argument, |l - max| 2^-24, which the subtraction has too.
+        // softmax: p = exp(l - max) / sum.  Sigmoid scores: l becomes score / sum of
+        // scores.  Where all of a token's scores are small (largest logit m below -20) they
+        // are taken in units of e^m: score e^-m = 1 / (e^m + e^(m - l)), which neither
+        // underflows nor meets an infinite sum; above, m = 0 and the exponent's argument
+        // is the logit itself.  1 - score is e^(m - l) times that where the score is near
+        // 1, so that a saturated expert's gradient keeps its digits.
         mx = group_max<L>(mx);
+        const float m = SIG && mx < -20.f ? mx : 0.f, em = SIG ? expf(m) : 1.f;
         float se = 0.f, sg = 0.f, c = 0.f, one_less[kBalPer];
 #pragma unroll
         for (int j = 0; j < kBalPer; ++j) {
-            p[j] = __expf(l[j] - mx);  // 0 for the lanes' places behind E, which hold -inf
+            p[j] = expf(l[j] - mx);  // 0 for the lanes' places behind E, which hold -inf
             se += p[j];
             if (SIG) {
-                const float sc = __fdividef(1.f, 1.f + __expf(-l[j]));
+                const float t = expf(m - l[j]), sc = 1.f / (em + t);
+                one_less[j] = l[j] > 0.f ? t * sc : 1.f - em * sc;
                 l[j] = sc;
-                one_less[j] = 1.f - sc;
                 sg += sc;
             }
             c = fmaf(f[j], SIG ? l[j] : p[j], c);
@@ -368,8 +372,8 @@ template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThrea
         se = group_sum<L>(se);
         c = group_sum<L>(c);
         if (SIG) sg = group_sum<L>(sg);
-        const float lse = mx + logf(se), inv_se = __fdividef(1.f, se);
-        const float inv_sg = SIG ? __fdividef(1.f, sg) : 0.f;
+        const float lse = mx + logf(se), inv_se = 1.f / se;
+        const float inv_sg = SIG ? 1.f / sg : 0.f;
         c *= SIG ? inv_sg : inv_se;
         if (t >= t1) continue;
         if (i >= 0 && lg == 0) {

@@ -75,3 +75,82 @@ def test_rmsnorm_range(scale, eps, T, D, dt):
     v = q.view(torch.float8_e4m3fn).double().unflatten(-1, (-1, 32)) * torch.exp2(qs.double() - 127)[..., None]
     step = torch.exp2(qs.double() - 127).repeat_interleave(32, 1)
     within(v.flatten(-2), n, 2.0**-4 * n.double().abs() + 2.0**-10 * step, "values")
+
+
+# ------------------------------------------------------------------- balance --
+
+def _balance(logits, ids, starts, score, cb, cz):
+    T, E = logits.shape
+    S = len(starts) - 1
+    cfg = M.MoeConfig.make(T, 8, 8, E, ids.shape[1], "bf16", score_func=score)
+    ws = torch.zeros(M.balance_workspace_size(cfg, S), dtype=torch.uint8, device="cuda")
+    out = (torch.empty(S, E, dtype=torch.int32, device="cuda"), torch.empty(2, device="cuda"),
+           torch.empty(S, device="cuda"), torch.empty(T, E, device="cuda"))
+    M.moe_balance_loss(cfg, logits, ids, torch.tensor(starts, dtype=torch.int32, device="cuda"), out[0], out[1], out[2],
+                       ws, dlogits=out[3], c_balance=cb, c_z=cz)
+    assert B.moe_get_device_status(ws) == 0
+    return out
+
+
+def _balance_ref(logits, ids, starts, score, cb, cz):
+    """(seq_loss, dlogits, magnitude of the gradient's terms) in 64 bits, from the
+    formulas; every token counts."""
+    T, E = logits.shape
+    K, S = ids.shape[1], len(starts) - 1
+    l = logits.double()
+    soft, lse = torch.softmax(l, 1), torch.logsumexp(l, 1, keepdim=True)
+    s = torch.sigmoid(l)
+    p, dp = (soft, soft) if score == "softmax" else (s / s.sum(1, keepdim=True),) * 2
+    if score != "softmax":
+        dp = p * torch.sigmoid(-l)
+    seq, d, mag = [], torch.zeros_like(l), torch.zeros_like(l)
+    for a, b in zip(starts[:-1], starts[1:]):
+        f = torch.bincount(ids[a:b].flatten().long(), minlength=E).double() / ((b - a) * K)
+        c = (p[a:b] * f).sum(1, keepdim=True)
+        seq.append(E * c.mean())
+        k = cb * E / (S * (b - a))
+        d[a:b], mag[a:b] = k * dp[a:b] * (f - c), abs(k) * dp[a:b] * (f + c)
+    d, mag = d + cz * 2 * lse / T * soft, mag + abs(cz) * 2 * lse.abs() / T * soft
+    return torch.stack(seq), d, mag
+
+
+# An element of the gradient is off by at most 2^-18 of its terms: two exponentials to
+# 2^-22 and the rounding of their arguments, sums of 8 + 5 terms and some ten
+# products and quotients at 2^-24 each.
+GRAD = 2.0**-18
+
+
+def _ids(g, T, E, K):
+    return torch.rand(T, E, generator=g, device="cuda").topk(K, 1).indices.to(torch.int32).contiguous()
+
+
+@pytest.mark.parametrize("E,K", [(8, 2), (17, 3), (64, 6), (256, 8)])
+@pytest.mark.parametrize("level,spread", [(-4, 1), (-19.5, 1), (-20.5, 1), (-60, 1), (-88, 0.3), (-88, 12), (-120, 5), (-300, 1),
+                                          (12, 2), (25, 3), (60, 1), (0, 25)])
+def test_balance_sigmoid_levels(level, spread, E, K):
+    """Sigmoid scores of logits far from zero: their shares of a token's sum are
+    what they are however small all of them get, and the gradient of a saturated
+    score is its own size, p (1 - sigmoid), not a difference of numbers near 1."""
+    g = _gen(E + 7)
+    T = 300
+    logits = level + spread * (2 * torch.rand(T, E, generator=g, device="cuda") - 1)
+    ids = _ids(g, T, E, K)
+    starts = [0, 120, 300]
+    counts, losses, seq, d = _balance(logits, ids, starts, "sigmoid", 0.01, 0.0)
+    rs, rd, mag = _balance_ref(logits, ids, starts, "sigmoid", 0.01, 0.0)
+    within(seq, rs, 2.0**-18 * rs, "seq_loss")
+    within(d, rd, GRAD * mag + 1e-38, "dlogits")
+
+
+@pytest.mark.parametrize("score,level", [("sigmoid", -4.0), ("sigmoid", -10.0), ("sigmoid", -60.0), ("softmax", -10.0)])
+def test_balance_gradient_is_fp32s(score, level):
+    """Root mean square of the gradient's error: some fifteen independent roundings
+    of 2^-24 / sqrt(3) each are 2^-22.8 of its terms, an exponential's ulp beside
+    them; held to twice 2^-22."""
+    g = _gen(6)
+    T, E, K = 2000, 64, 4
+    logits, ids = level + _randn(g, T, E), _ids(g, T, E, K)
+    *_, d = _balance(logits, ids, [0, T], score, 0.01, 0.0)
+    _, rd, mag = _balance_ref(logits, ids, [0, T], score, 0.01, 0.0)
+    rms = float(((d.double() - rd) / mag).square().mean().sqrt())
+    assert rms <= 2.0**-21
