@@ -14,10 +14,11 @@
 // the gradient needs first, come from the ids alone.
 //
 // Sums do not depend on the order of the blocks: counts are integers; a
-// sequence's c_t, each in [0, 1], are added as integers of 2^-32 (half a step,
-// 2^-33, is far below fp32's own rounding of a c_t near 1/E >= 2^-8); z is summed
-// per thread and block in fp64 and the blocks' sums are added in order by the
-// block that finishes last.
+// sequence's c_t, each in [0, 1], are added as integers of 2^-(63 - b), b the bits
+// of T, the finest unit whose sum over T tokens cannot overflow.  A c_t, an fp32
+// number, is held exactly from 2^(b - 40) on, and to half a unit below: seq_loss
+// is off by at most E 2^-(64 - b).  z is summed per thread and block in fp64 and the
+// blocks' sums are added in order by the block that finishes last.
 //
 // One cooperative launch (every block resident): zero the results, count, and the
 // gradient, with two grid barriers between them.  Both are split: a block
@@ -41,7 +42,6 @@ constexpr int kBalPer = 8;          // experts per lane: E <= 256
 constexpr int kBalStarts = 2048;    // sequence borders held in shared memory, else searched in global
 constexpr int kBalHist = 4096;      // (sequence, expert) counters of a block's tokens
 constexpr int kBalSpan = 512;       // and sequences
-constexpr double kBalFix = 4294967296.0;  // 2^32
 
 // Scratch of a call, laid out by balance_layout.
 struct BalScratch {
@@ -50,7 +50,7 @@ struct BalScratch {
     uint32_t* done;           // blocks that have finished (zero between calls)
     int* tokens;              // (S) n_i
     int* bad;                 // (S) a counted token's c_t is not a number
-    unsigned long long* acc;  // (S) sum of c_t in 2^-32
+    unsigned long long* acc;  // (S) sum of c_t in units of 1 / fix
     double* zpart;            // per block: sum of lse^2
 };
 
@@ -66,6 +66,7 @@ struct BalArgs {
     int64_t T, chunk;  // tokens, tokens per block
     int E, K, S;
     float c_balance, c_z;
+    float fix;          // 2^(63 - b), T < 2^b
     BalScratch w;
 };
 
@@ -378,7 +379,7 @@ template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThrea
         if (t >= t1) continue;
         if (i >= 0 && lg == 0) {
             z = fma((double)lse, (double)lse, z);
-            if (c >= 0.f && c <= 1.5f) acc += __float2ull_rn(c * (float)kBalFix);  // exact but for the rounding
+            if (c >= 0.f && c <= 1.5f) acc += __float2ull_rn(c * a.fix);  // (the product is exact)
             else a.w.bad[i] = 1;
         }
         if (a.dlogits != nullptr) {
@@ -424,7 +425,7 @@ template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThrea
         const int n = __ldcg(&a.w.tokens[k]), bad = __ldcg(&a.w.bad[k]);
         const unsigned long long sum = __ldcg(&a.w.acc[k]);
         double v = 0.0;
-        if (n > 0) v = bad ? (double)NAN : (double)E * (1.0 / kBalFix) * (double)sum / (double)n;
+        if (n > 0) v = bad ? (double)NAN : (double)E * (double)sum / (double)a.fix / (double)n;
         a.seq_loss[k] = (float)v;
         bsum += v;
     }
@@ -514,6 +515,9 @@ cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, 
     a.T = c.T; a.chunk = 0; a.E = c.E; a.K = c.K; a.S = (int)S;
     const bool sigmoid = c.score_func == MOE_SCORE_SIGMOID;
     a.c_balance = c_balance; a.c_z = c_z;
+    int bits = 0;
+    while (c.T >> bits != 0) ++bits;
+    a.fix = ldexpf(1.f, 63 - bits);
     a.w.status = reinterpret_cast<int*>(w + L.head);
     a.w.bar = reinterpret_cast<uint32_t*>(w + L.head + 64);
     a.w.done = reinterpret_cast<uint32_t*>(w + L.head + 128);

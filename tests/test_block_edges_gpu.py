@@ -110,7 +110,10 @@ def _balance_ref(logits, ids, starts, score, cb, cz):
         seq.append(E * c.mean())
         k = cb * E / (S * (b - a))
         d[a:b], mag[a:b] = k * dp[a:b] * (f - c), abs(k) * dp[a:b] * (f + c)
-    d, mag = d + cz * 2 * lse / T * soft, mag + abs(cz) * 2 * lse.abs() / T * soft
+    # lse is the sum of the largest logit and a logarithm, either sign each: its error
+    # goes by 2^-24 of those two, which may cancel to a smaller lse
+    top = l.amax(1, keepdim=True)
+    d, mag = d + cz * 2 * lse / T * soft, mag + abs(cz) * 2 * (top.abs() + (lse - top)) / T * soft
     return torch.stack(seq), d, mag
 
 
@@ -154,3 +157,22 @@ def test_balance_gradient_is_fp32s(score, level):
     _, rd, mag = _balance_ref(logits, ids, [0, T], score, 0.01, 0.0)
     rms = float(((d.double() - rd) / mag).square().mean().sqrt())
     assert rms <= 2.0**-21
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,gap", [(1, 20), (60, 15), (60, 22), (3000, 18), (70001, 14)])
+def test_balance_loss_of_experts_against_their_scores(T, gap, score):
+    """Ids that a selection bias turned against the scores: a token's share of the
+    loss is a small number, and the loss keeps its digits.  A share is held in units
+    of 2^-(63 - b), b the bits of T."""
+    g = _gen(T)
+    E, K = 16, 2
+    logits = _randn(g, T, E) - 3
+    logits[:, 4:8] -= gap
+    ids = (4 + _ids(g, T, 4, K)).contiguous()
+    starts = [0, T // 3, T] if T > 2 else [0, T]
+    counts, losses, seq, d = _balance(logits, ids, starts, score, 0.01, 0.001)
+    rs, rd, mag = _balance_ref(logits, ids, starts, score, 0.01, 0.001)
+    within(seq, rs, 2.0**-18 * rs + E * 2.0**-(64 - T.bit_length()), "seq_loss")
+    within(losses[1], rs.mean(), 2.0**-18 * rs.mean() + E * 2.0**-(64 - T.bit_length()), "balance")
+    within(d, rd, GRAD * mag + 1e-38, "dlogits")
