@@ -260,23 +260,30 @@ MOE_DEVICE void build_tiles(Misc* m, const Args& a, int bm)
 }
 
 // Scales of stages 4g .. 4g+3 of one row (null: zeros), nb = bytes per row.
-// Rows are 16-byte, 4-byte or only byte aligned with nb.
-MOE_DEVICE uint4 load_scales(const uint8_t* row, int g, int nb)
+// Rows are 16-byte, 4-byte or only byte aligned with nb.  WEIGHT: of a weight, which
+// nothing writes while the kernel runs (the read-only path).  The rows' scales of the
+// down product are written by the gate/up product while this kernel is already
+// resident: ordinary loads, which the wait for that product orders.
+template <bool WEIGHT, typename V> MOE_DEVICE V load_scale(const uint8_t* p)
+{
+    return WEIGHT ? __ldg(reinterpret_cast<const V*>(p)) : *reinterpret_cast<const V*>(p);
+}
+template <bool WEIGHT> MOE_DEVICE uint4 load_scales(const uint8_t* row, int g, int nb)
 {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (row == nullptr) return v;
-    if ((nb & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(row) + g);
+    if ((nb & 15) == 0) return load_scale<WEIGHT, uint4>(row + 16 * g);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int at = 16 * g + 4 * i;
         w[i] = 0;
         if ((nb & 3) == 0) {
-            if (at < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + at));
+            if (at < nb) w[i] = load_scale<WEIGHT, uint32_t>(row + at);
         } else {
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (at + b < nb) w[i] |= (uint32_t)__ldg(row + at + b) << (8 * b);
+                if (at + b < nb) w[i] |= (uint32_t)load_scale<WEIGHT, uint8_t>(row + at + b) << (8 * b);
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -552,9 +559,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         auto load_next = [&](int i2) {
             if (ld_t >= total) return;
             if (ld_g == 0) rows_of(ld_t);
-            va[i2] = load_scales(pa, ld_g, nb);
-            v0[i2] = load_scales(pb0, ld_g, nb);
-            v1[i2] = load_scales(pb1, ld_g, nb);
+            va[i2] = load_scales<false>(pa, ld_g, nb);
+            v0[i2] = load_scales<true>(pb0, ld_g, nb);
+            v1[i2] = load_scales<true>(pb1, ld_g, nb);
             if (++ld_g == groups) {
                 ld_g = 0;
                 ld_t += units;
@@ -970,10 +977,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int ld_t = unit, ld_g = unit < total ? first_group(unit % splits) : 0;
         bool fresh = true;
         auto load_weights = [&](int i2) {
-            v0[i2] = load_scales(pw0, ld_g, nb);
-            v1[i2] = load_scales(pw1, ld_g, nb);
+            v0[i2] = load_scales<true>(pw0, ld_g, nb);
+            v1[i2] = load_scales<true>(pw1, ld_g, nb);
         };
-        auto load_tokens = [&](int i2) { vx[i2] = load_scales(px, ld_g, nb); };
+        auto load_tokens = [&](int i2) { vx[i2] = load_scales<false>(px, ld_g, nb); };
         auto load_next = [&](int i2) {
             if (ld_t >= total) return;
             if (fresh) rows_of(ld_t);

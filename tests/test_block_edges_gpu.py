@@ -176,3 +176,47 @@ def test_balance_loss_of_experts_against_their_scores(T, gap, score):
     within(seq, rs, 2.0**-18 * rs + E * 2.0**-(64 - T.bit_length()), "seq_loss")
     within(losses[1], rs.mean(), 2.0**-18 * rs.mean() + E * 2.0**-(64 - T.bit_length()), "balance")
     within(d, rd, GRAD * mag + 1e-38, "dlogits")
+
+
+# ------------------------------------------------------------- 8-bit experts --
+
+def _mx8(v):
+    """v (.., n) as e4m3 blocks of 32 under power-of-two scales (any valid pair will do)."""
+    b = v.unflatten(-1, (-1, 32))
+    e = torch.ceil(torch.log2(b.abs().amax(-1).clamp(min=1e-30) / 448)).clamp(-126, 127)
+    return (b / torch.exp2(e)[..., None]).to(torch.float8_e4m3fn).flatten(-2), (e + 127).to(torch.uint8)
+
+
+# pairs, single CTAs, few rows, few rows with the down product in parts
+@pytest.mark.parametrize("T,D,F,E,K", [(400, 256, 192, 2, 2), (100, 224, 160, 4, 2), (30, 256, 192, 8, 2), (2, 256, 4096, 8, 2)])
+def test_experts_mx8_see_the_rows_of_their_own_call(T, D, F, E, K):
+    """Calls in a row on the same buffers with other rows each time: every call's
+    output is its own rows', bit for bit (the down product starts under the end of
+    the product that writes what it reads)."""
+    g = _gen(T)
+    R = T * K
+    counts = torch.bincount(_ids(g, T, E, K).flatten().long(), minlength=E)
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+    w = []
+    for n, k in ((F, D), (F, D), (D, F)):
+        w += list(_mx8(0.05 * _randn(g, E, n, k)))
+    rows = [_mx8(s * _randn(g, R, D)) for s in (1.0, 30.0, 0.01)]
+    cfg = M.MoeConfig.make(T, D, F, E, K, "bf16")
+    xq, xs = torch.empty_like(rows[0][0]), torch.empty_like(rows[0][1])
+    hq, hs = torch.empty(R, F, dtype=torch.uint8, device="cuda"), torch.empty(R, F // 32, dtype=torch.uint8, device="cuda")
+    y, ws = torch.empty(R, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(M.mx8_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+
+    def call(i):
+        xq.view(torch.uint8).copy_(rows[i][0].view(torch.uint8))
+        xs.copy_(rows[i][1])
+        M.moe_expert_ffn_mx8(cfg, xq, xs, offsets, None, None, w, hq, hs, y, ws)
+        return y.clone(), hs.clone()
+    want = []
+    for i in range(3):
+        want.append(call(i))
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0][1], want[1][1])
+    got = [call(i % 3) for i in range(60)]
+    for i, (yi, hi) in enumerate(got):
+        assert torch.equal(yi, want[i % 3][0]) and torch.equal(hi, want[i % 3][1]), i
+    assert B.moe_get_device_status(ws) == 0
