@@ -302,9 +302,15 @@ MOE_DEVICE void store32(void* p, const uint32_t* v)
                  : "memory");
 }
 
-// silu(g) u in fp32: the exponential and the quotient to 2^-21, so that the one
-// rounding of h is the 8-bit one.
-MOE_DEVICE float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) u in fp32: g u / (1 + e^-g) for g >= 0, g e^g u / (1 + e^g) below, so that the
+// divisor stays in 1 .. 2 (from e^87 on the fast quotient gives 0, and a large u would
+// have shown it).  The exponential errs by 2 + 1.2 |g| units of 2^-23 at most, the quotient
+// by 2: 2^-20 of the value up to |g| = 3, 2^-18 up to 20; h is then rounded to 2^-4.
+MOE_DEVICE float swiglu(float g, float u)
+{
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g < 0.f ? g * e : g, 1.0f + e) * u;
+}
 
 template <bool GATEUP, bool PAIR>
 __global__ void __launch_bounds__(NUM_THREADS, 1)

@@ -220,3 +220,37 @@ def test_experts_mx8_see_the_rows_of_their_own_call(T, D, F, E, K):
     for i, (yi, hi) in enumerate(got):
         assert torch.equal(yi, want[i % 3][0]) and torch.equal(hi, want[i % 3][1]), i
     assert B.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T,E", [(400, 1), (60, 1), (20, 1)])  # pairs, single CTAs, few rows
+def test_experts_mx8_silu_far_below_zero(T, E):
+    """Gates from -87 on, where e^-g passes 2^126, beside values that make g e^g u a
+    number of ordinary size: h is silu(g) u, to its own rounding of 2^-4 (or half its
+    block's least step) and that of e^g, a denormal number (half a step, 2^-150)."""
+    D, F = 32, 64
+    gates = torch.linspace(-86.5, -95, T, device="cuda")
+    x = torch.zeros(T, D, device="cuda")
+    x[:, 0] = 1
+    x[:, 1] = torch.floor(-gates)          # 1.0 x whole part and 1.0 x a fraction of it, both exact in 8 bits
+    x[:, 1] = (x[:, 1] / 8).floor() * 8    # 80, 88
+    x[:, 2] = ((-gates - x[:, 1]).clamp(0, 8) * 2).round() / 2
+    xq, xs = _mx8(x)
+    xv = (xq.double().unflatten(-1, (-1, 32)) * torch.exp2(xs.double() - 127)[..., None]).flatten(-2)
+    gate, up, down = torch.zeros(E, F, D, device="cuda"), torch.zeros(E, F, D, device="cuda"), torch.zeros(E, D, F, device="cuda")
+    gate[:, :, 1] = gate[:, :, 2] = -1
+    up[:, :, 0] = 2.0**120 * (1 + torch.arange(F, device="cuda") % 7)
+    w = [t for v in (gate, up, down) for t in _mx8(v)]
+    cfg = M.MoeConfig.make(T, D, F, E, 1, "bf16")
+    hq, hs = torch.empty(T, F, dtype=torch.uint8, device="cuda"), torch.empty(T, F // 32, dtype=torch.uint8, device="cuda")
+    y, ws = torch.empty(T, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(M.mx8_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    offsets = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    M.moe_expert_ffn_mx8(cfg, xq, xs, offsets, None, None, w, hq, hs, y, ws)
+    assert B.moe_get_device_status(ws) == 0
+    g = xv @ gate[0].double().T
+    assert float(g.min()) < -94 and float(g.max()) > -88
+    h = g * torch.sigmoid(g) * (xv @ up[0].double().T)
+    step = torch.exp2(hs.double() - 127).repeat_interleave(32, 1)
+    got = hq.view(torch.float8_e4m3fn).double() * step
+    # the fast exponential, 2 + 1.2 |g| units of 2^-23, and its own half step
+    eh = h.abs() * ((4 + 1.2 * g.abs()) * 2.0**-23 + 2.0**-150 / torch.exp(g))
+    within(got, h, 2.0**-4 * (h.abs() + eh) + 2.0**-10 * step + eh, "h")
