@@ -476,7 +476,8 @@ typedef struct moe_mx8_weights {
 } moe_mx8_weights;
 
 /* Bytes of device workspace moe_expert_ffn_mx8 needs (256-byte aligned, zeroed
- * once before first use; its first word is the device status word). */
+ * once before first use; its first word is the device status word).  They do not
+ * fall with T: the workspace of a larger batch serves a smaller one. */
 MOE_API moe_status moe_mx8_workspace_size(const moe_config *cfg, size_t *bytes);
 
 /*

@@ -1314,10 +1314,21 @@ static int few_splits(const moe_config& c, int64_t max_rows)
     return n > 1 ? (int)n : 1;
 }
 
+// Scratch for the parts of every number of rows up to max_rows, so that a workspace of
+// a larger batch serves a smaller one: n parts are cut for at most the rows whose tiles,
+// min(rows, E + rows / 32) n_tiles, fit 148 / n times.
 size_t mx8_part_bytes(const moe_config& c, int64_t max_rows)
 {
-    const int n = few_splits(c, max_rows);
-    return n > 1 ? (size_t)n * (size_t)max_rows * c.D * sizeof(float) : 0;
+    const int64_t n_tiles = (c.D + 255) / 256, most = ((c.F + 511) / 512) / 2 < 8 ? ((c.F + 511) / 512) / 2 : 8;
+    const int64_t few = max_rows < mx::kFewRows * (int64_t)c.E ? max_rows : mx::kFewRows * (int64_t)c.E;
+    int64_t rows = 0;  // the most of n times its rows
+    for (int64_t n = 2; n <= most; ++n) {
+        const int64_t q = 148 / n / n_tiles;
+        const int64_t fit = q < c.E ? q : 32 * (q - c.E) + 31 > q ? 32 * (q - c.E) + 31 : q;
+        const int64_t r = fit < few ? fit : few;
+        if (n * r > rows) rows = n * r;
+    }
+    return (size_t)rows * c.D * sizeof(float);
 }
 
 cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq, const void* xs,

@@ -269,7 +269,7 @@ cudaError_t launch_ffn_mx8(const moe_config& c, int64_t max_rows, const void* xq
                            const int32_t* offsets, const int32_t* perm, const float* topk_w,
                            const moe_mx8_weights& w, void* hq, void* hs, void* y_perm, void* amaps, void* part,
                            int* status, cudaStream_t s);
-// Scratch of launch_ffn_mx8's `part` (0: none).
+// Scratch of launch_ffn_mx8's `part` for up to max_rows rows (0: none).
 size_t mx8_part_bytes(const moe_config& c, int64_t max_rows);
 size_t balance_bytes(const moe_config& c, int64_t S);
 cudaError_t launch_balance(const moe_config& c, int64_t S, const float* logits, const int32_t* ids,

@@ -31,3 +31,25 @@ def test_rows_scales_are_not_read_through_the_read_only_path():
         assert how == ("<false>" if what in ("pa", "px") else "<true>"), what
     assert [line.strip() for line in text.splitlines() if "__ldg(" in line] == [
         "return WEIGHT ? __ldg(reinterpret_cast<const V*>(p)) : *reinterpret_cast<const V*>(p);"]
+
+
+def _parts(T, D, F, E, K):
+    """(parts, rows) of the down product's contracted axis, from the rule: rows of few
+    tokens an expert, tiles that leave SMs idle, two groups of 512 a part at least."""
+    R = T * K
+    if R > 24 * E:
+        return 1, R
+    tiles = min(R, E + R // 32) * -(-D // 256)
+    return max(1, min(148 // tiles, 8, -(-F // 512) // 2)), R
+
+
+@pytest.mark.parametrize("D,F,E,K", [(4096, 14336, 8, 2), (256, 4096, 8, 2), (256, 8192, 1, 1), (96, 8192, 4, 1),
+                                     (2048, 1408, 64, 6), (7168, 2048, 256, 8), (32, 16384, 2, 2), (512, 2080, 40, 1)])
+def test_mx8_workspace_of_a_larger_batch_serves_a_smaller_one(lib, D, F, E, K):
+    last = 0
+    for T in list(range(1, 300)) + [512, 1000, 3000, 10000, 70000]:
+        size = B.mx8_workspace_size(B.MoeConfig.make(T, D, F, E, K, "bf16"))
+        n, R = _parts(T, D, F, E, K)
+        need = 256 + -(-2 * E * 128 // 256) * 256 + (n * R * D * 4 if n > 1 else 0)
+        assert size >= max(last, need), T
+        last = size

@@ -254,3 +254,27 @@ def test_experts_mx8_silu_far_below_zero(T, E):
     # the fast exponential, 2 + 1.2 |g| units of 2^-23, and its own half step
     eh = h.abs() * ((4 + 1.2 * g.abs()) * 2.0**-23 + 2.0**-150 / torch.exp(g))
     within(got, h, 2.0**-4 * (h.abs() + eh) + 2.0**-10 * step + eh, "h")
+
+
+def test_experts_mx8_one_workspace_for_every_batch():
+    """The workspace of the largest batch through all of them, forms in turn: the bits
+    of calls with workspaces of their own."""
+    D, F, E, K = 256, 4096, 4, 2
+    g = _gen(2)
+    w = [t for n, k in ((F, D), (F, D), (D, F)) for t in _mx8(0.05 * _randn(g, E, n, k))]
+    size = M.mx8_workspace_size(M.MoeConfig.make(600, D, F, E, K, "bf16"))
+    shared = torch.zeros(size + 4096, dtype=torch.uint8, device="cuda")
+    shared[size:] = 77
+    for T in (600, 1, 20, 3, 100, 2, 47, 600):
+        cfg, R = M.MoeConfig.make(T, D, F, E, K, "bf16"), T * K
+        counts = torch.bincount(_ids(g, T, E, K).flatten().long(), minlength=E)
+        offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+        xq, xs = _mx8(_randn(g, R, D))
+        hq, hs = torch.empty(R, F, dtype=torch.uint8, device="cuda"), torch.empty(R, F // 32, dtype=torch.uint8, device="cuda")
+        y = [torch.empty(R, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        own = torch.zeros(M.mx8_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        for out, ws in zip(y, (own, shared[:size])):
+            M.moe_expert_ffn_mx8(cfg, xq, xs, offsets, None, None, w, hq, hs, out, ws)
+            assert B.moe_get_device_status(ws) == 0
+        assert torch.equal(*y)
+    assert bool((shared[size:] == 77).all())
