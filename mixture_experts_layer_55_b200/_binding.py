@@ -343,9 +343,10 @@ def moe_backward(cfg, x, w_router, w_gate, w_up, w_down, state, dy, dx, dw_route
     gradient buffers when cfg.F_shared > 0.  dlogits_add (T, E) fp32: a further
     gradient of the routing logits (moe_balance_loss's)."""
     if dlogits_add is not None:
-        import torch
-        if dlogits_add.dtype != torch.float32 or dlogits_add.numel() != cfg.T * cfg.E:
-            raise ValueError("moe_backward: dlogits_add must be (T, E) fp32")
+        specs = [("dlogits_add", dlogits_add, _types()[1], cfg.T * cfg.E)]
+        if isinstance(state, _TENSOR):  # on the state's device
+            specs.append(("state", state, (state.dtype,), state.numel()))
+        _check_tensors("moe_backward", specs)
     sg, su, sd = shared if shared is not None else (None, None, None)
     dg, du, dd = dshared if dshared is not None else (None, None, None)
     st = lib().moe_backward_aux(_cfg(cfg), _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up),

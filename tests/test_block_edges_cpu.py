@@ -53,3 +53,20 @@ def test_mx8_workspace_of_a_larger_batch_serves_a_smaller_one(lib, D, F, E, K):
         need = 256 + -(-2 * E * 128 // 256) * 256 + (n * R * D * 4 if n > 1 else 0)
         assert size >= max(last, need), T
         last = size
+
+
+def test_dlogits_add_is_checked_like_every_tensor(lib):
+    """A host tensor, a transposed one or one on another device than the state never
+    reaches a kernel as an address."""
+    c = B.MoeConfig.make(4, 64, 64, 8, 2, "bf16")
+    state = torch.zeros(16, dtype=torch.uint8)
+    for args in (dict(), dict(state=state)):
+        rest = dict.fromkeys(("x", "w_router", "w_gate", "w_up", "w_down", "state", "dy", "dx", "dw_router", "dw_gate",
+                              "dw_up", "dw_down", "workspace"))
+        rest.update(args)
+        with pytest.raises(ValueError, match="CUDA device"):
+            B.moe_backward(c, **rest, dlogits_add=torch.zeros(4, 8))
+        with pytest.raises(ValueError, match="contiguous"):
+            B.moe_backward(c, **rest, dlogits_add=torch.zeros(8, 4).t())
+        with pytest.raises(ValueError, match="dlogits_add must be a tensor"):
+            B.moe_backward(c, **rest, dlogits_add=[0.0] * 32)
