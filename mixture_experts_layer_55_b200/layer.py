@@ -117,10 +117,19 @@ class MoELayer:
                           counts=self.counts if stats else None, stream=stream)
         return y
 
-    def _norm(self, x, residual, bits8=False, keep=False):
+    def _check_rows(self, where, logit_noise=None, **rows):
+        """The block's tensors are whole (T, D) batches of the layer's type on its device."""
+        T, D, E = self.cfg.T, self.cfg.D, self.cfg.E
+        specs = [(name, t, (self.torch_dtype,), T * D) for name, t in rows.items()]
+        specs.append(("logit_noise", logit_noise, (torch.float32,), T * E))
+        specs.append(("the layer's workspace", self.workspace, (torch.uint8,), self.workspace.numel()))
+        B._check_tensors(where, specs)
+
+    def _norm(self, where, x, residual, y, logit_noise, bits8=False, keep=False):
         """moe_rmsnorm into new buffers: (n, s, q, q_scales, rstd)."""
         if self.norm_weight is None:
             raise ValueError("the layer has no norm_weight")
+        self._check_rows(where, logit_noise, x=x, residual=residual, y=y)
         n = torch.empty_like(x)
         s = torch.empty_like(x) if residual is not None else None
         q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if bits8 else None
@@ -134,7 +143,7 @@ class MoELayer:
         """The pre-norm block: s = x + residual, y = MoE(norm(s)); returns (y, s),
         which the next block takes as its x and residual.  With 8-bit experts
         the norm writes the rows they read.  On the current stream."""
-        n, s, q, qs, _ = self._norm(x, residual, bits8=self.mx8 is not None)
+        n, s, q, qs, _ = self._norm("forward_block", x, residual, y, logit_noise, bits8=self.mx8 is not None)
         if y is None:
             y = torch.empty_like(x)
         if self.mx8 is not None:
@@ -244,7 +253,7 @@ class MoELayer:
         """forward_block() that keeps what backward_block() reads; returns (y, s)."""
         if self.mx8 is not None:
             raise ValueError("8-bit experts are for inference: train a layer without them")
-        n, s, _, _, rstd = self._norm(x, residual, keep=True)
+        n, s, _, _, rstd = self._norm("forward_block_train", x, residual, y, logit_noise, keep=True)
         y = self.forward_train(n, y, logit_noise=logit_noise)
         self._block = (s, rstd)
         return y, s
@@ -257,6 +266,7 @@ class MoELayer:
         if getattr(self, "_block", None) is None:
             raise RuntimeError("backward_block() needs a forward_block_train() first")
         s, rstd = self._block
+        self._check_rows("backward_block", dy=dy, ds=ds)
         grads = self.backward(dy, c_balance, c_z, grads, dlogits_add=dlogits_add)
         if "dgamma" not in grads:
             grads["dgamma"] = torch.empty(s.shape[1], dtype=torch.float32, device=s.device)

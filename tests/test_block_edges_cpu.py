@@ -70,3 +70,32 @@ def test_dlogits_add_is_checked_like_every_tensor(lib):
             B.moe_backward(c, **rest, dlogits_add=torch.zeros(8, 4).t())
         with pytest.raises(ValueError, match="dlogits_add must be a tensor"):
             B.moe_backward(c, **rest, dlogits_add=[0.0] * 32)
+
+
+def _layer(T=4, D=64, F=64, E=2, **kw):
+    w = [torch.zeros(E, D, F, dtype=torch.bfloat16) for _ in range(2)] + [torch.zeros(E, F, D, dtype=torch.bfloat16)]
+    return MoELayer(T, torch.zeros(D, E), *w, K=1, norm_weight=torch.ones(D), **kw)
+
+
+def test_block_refuses_what_is_not_a_whole_batch(lib):
+    """A batch of fewer rows, another type or layout would be read or written out of
+    range by the layer's kernels: each is refused by name, before any device work."""
+    layer = _layer()
+    good = torch.zeros(4, 64, dtype=torch.bfloat16)
+    bad = {"elements": torch.zeros(3, 64, dtype=torch.bfloat16), "dtype": torch.zeros(4, 64),
+           "contiguous": torch.zeros(64, 4, dtype=torch.bfloat16).t(), "must be a tensor": [1.0]}
+    for call, names in ((layer.forward_block, ("x", "residual", "y")), (layer.forward_block_train, ("x", "residual", "y"))):
+        for name in names:
+            for what, t in bad.items():
+                args = {"x": good, name: t}
+                with pytest.raises(ValueError, match=f"{call.__name__}: {name} .*{what}"):
+                    call(**args)
+        with pytest.raises(ValueError, match="logit_noise has 7 elements"):
+            call(good, logit_noise=torch.zeros(7))
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(good)
+    layer._block = (good, torch.ones(4))
+    for name in ("dy", "ds"):
+        for what, t in bad.items():
+            with pytest.raises(ValueError, match=f"backward_block: {name} .*{what}"):
+                layer.backward_block(**{"dy": good, name: t})
