@@ -12,6 +12,11 @@ import torch
 from . import _binding as B
 
 
+def _same(a, b) -> bool:
+    """Both are tensors, and start at the same address."""
+    return isinstance(a, torch.Tensor) and isinstance(b, torch.Tensor) and a.data_ptr() == b.data_ptr()
+
+
 class MoELayer:
     """Token-choice top-k MoE layer (forward and backward)
     on one CUDA device.
@@ -129,6 +134,8 @@ class MoELayer:
         """moe_rmsnorm into new buffers: (n, s, q, q_scales, rstd)."""
         if self.norm_weight is None:
             raise ValueError("the layer has no norm_weight")
+        if residual is None and _same(x, y):
+            raise ValueError(f"{where}: y must not be x, which is the sum the call returns")
         self._check_rows(where, logit_noise, x=x, residual=residual, y=y)
         n = torch.empty_like(x)
         s = torch.empty_like(x) if residual is not None else None
@@ -266,6 +273,8 @@ class MoELayer:
         if getattr(self, "_block", None) is None:
             raise RuntimeError("backward_block() needs a forward_block_train() first")
         s, rstd = self._block
+        if grads is not None and _same(ds, grads["dx"]):
+            raise ValueError("backward_block: ds must not be grads' dx, which is written before ds is read")
         self._check_rows("backward_block", dy=dy, ds=ds)
         grads = self.backward(dy, c_balance, c_z, grads, dlogits_add=dlogits_add)
         if "dgamma" not in grads:

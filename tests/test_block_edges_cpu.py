@@ -99,3 +99,21 @@ def test_block_refuses_what_is_not_a_whole_batch(lib):
         for what, t in bad.items():
             with pytest.raises(ValueError, match=f"backward_block: {name} .*{what}"):
                 layer.backward_block(**{"dy": good, name: t})
+
+
+def test_block_refuses_outputs_over_what_it_still_needs(lib):
+    """Without a residual x is the sum that the call returns and the backward reads: y
+    in its place is refused; so is a ds in the buffer that the layer's dx goes to."""
+    layer = _layer()
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (layer.forward_block, layer.forward_block_train):
+        with pytest.raises(ValueError, match="y must not be x"):
+            call(x, y=x)
+        with pytest.raises(ValueError, match="y must not be x"):
+            call(x, y=x.view(-1).view(4, 64))
+        with pytest.raises(ValueError, match="CUDA device"):  # over x or the residual beside a sum of its own: no
+            call(x, residual=torch.zeros_like(x), y=x)        # refusal but that of host tensors
+    layer._block = (x, torch.ones(4))
+    dx = torch.zeros_like(x)
+    with pytest.raises(ValueError, match="ds must not be"):
+        layer.backward_block(torch.zeros_like(x), ds=dx, grads={"dx": dx})

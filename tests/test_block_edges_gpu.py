@@ -278,3 +278,29 @@ def test_experts_mx8_one_workspace_for_every_batch():
             assert B.moe_get_device_status(ws) == 0
         assert torch.equal(*y)
     assert bool((shared[size:] == 77).all())
+
+
+# ------------------------------------------------------- the layer's own paths --
+
+def _layer(T, D, F, E, K, seed, dtype=torch.bfloat16, **kw):
+    g = _gen(seed)
+    wr = 0.1 * _randn(g, D, E)
+    w = [0.05 * _randn(g, E, D, F), 0.05 * _randn(g, E, D, F), 0.05 * _randn(g, E, F, D)]
+    return M.MoELayer(T, wr, *(v.to(dtype) for v in w), K, norm_weight=1 + 0.2 * _randn(g, D), **kw)
+
+
+@pytest.mark.parametrize("experts", [None, "mx8"])
+def test_block_outputs_over_its_inputs(experts):
+    """y over x or over the residual where the sum has a buffer of its own: the same
+    bits as into a fresh one."""
+    T, D = 90, 128
+    layer = _layer(T, D, 64, 4, 2, 1, experts=experts)
+    g = _gen(3)
+    x, res = _randn(g, T, D, dtype=torch.bfloat16), _randn(g, T, D, dtype=torch.bfloat16)
+    y, s = layer.forward_block(x, res)
+    for over in range(2):
+        a = [x.clone(), res.clone()]
+        y2, s2 = layer.forward_block(*a, y=a[over])
+        assert y2 is a[over] and torch.equal(y2, y) and torch.equal(s2, s)
+    with pytest.raises(ValueError):
+        layer.forward_block(x, y=x)
