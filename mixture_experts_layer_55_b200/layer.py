@@ -290,8 +290,9 @@ class MoELayer:
         """moe_balance_loss of the last forward_train's routing over the sequences
         seq_starts (S + 1) int32 and the tokens of token_mask: a dict of losses
         [z, balance], seq_loss (S), counts (S, E) and dlogits (T, E), the gradient
-        of c_balance * balance + c_z * z that backward() adds as dlogits_add.  On the
-        current stream."""
+        of c_balance * balance + c_z * z that backward() adds as dlogits_add.  Malformed
+        seq_starts show in the call's own workspace, also in the dict:
+        moe_get_device_status(result["workspace"]).  On the current stream."""
         if getattr(self, "_train_x", None) is None:
             raise RuntimeError("balance_loss() needs a forward_train() first")
         T, E, K, S = self.cfg.T, self.cfg.E, self.cfg.K, seq_starts.numel() - 1
@@ -301,7 +302,7 @@ class MoELayer:
         f32 = dict(dtype=torch.float32, device=self.device)
         ws = torch.zeros(B.balance_workspace_size(self.cfg, S), dtype=torch.uint8, device=self.device)
         out = dict(losses=torch.empty(2, **f32), seq_loss=torch.empty(S, **f32), dlogits=torch.empty(T, E, **f32),
-                   counts=torch.empty(S, E, dtype=torch.int32, device=self.device))
+                   counts=torch.empty(S, E, dtype=torch.int32, device=self.device), workspace=ws)
         B.moe_balance_loss(self.cfg, logits, ids, seq_starts, out["counts"], out["losses"], out["seq_loss"], ws,
                            token_mask=token_mask, dlogits=out["dlogits"], c_balance=c_balance, c_z=c_z)
         return out

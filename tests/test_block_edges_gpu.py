@@ -304,3 +304,21 @@ def test_block_outputs_over_its_inputs(experts):
         assert y2 is a[over] and torch.equal(y2, y) and torch.equal(s2, s)
     with pytest.raises(ValueError):
         layer.forward_block(x, y=x)
+
+
+def test_layer_balance_loss_shows_malformed_borders():
+    """The flag of a batch with malformed borders can be asked for, call by call; the
+    next call is clean."""
+    T, D = 40, 64
+    layer = _layer(T, D, 64, 4, 2, 5)
+    layer.forward_block_train(_randn(_gen(1), T, D, dtype=torch.bfloat16))
+    good = torch.tensor([0, 10, 40], dtype=torch.int32, device="cuda")
+    want = layer.balance_loss(good, c_balance=0.1)
+    assert B.moe_get_device_status(want["workspace"]) == 0
+    for starts in ([0, 30, 20], [0, 10, 41], [-1, 10, 40]):
+        bad = layer.balance_loss(torch.tensor(starts, dtype=torch.int32, device="cuda"), c_balance=0.1)
+        assert B.moe_get_device_status(bad["workspace"]) == B.MOE_DEVFLAG_BOUNDS
+    again = layer.balance_loss(good, c_balance=0.1)
+    assert B.moe_get_device_status(again["workspace"]) == 0
+    for k in ("losses", "seq_loss", "counts", "dlogits"):
+        assert torch.equal(again[k], want[k])
