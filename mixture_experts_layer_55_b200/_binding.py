@@ -512,9 +512,10 @@ def _types():
 def _ws(where, workspace):
     """The workspace's _check_tensors entry: any number of bytes (the library says
     whether they are enough)."""
-    if workspace is None:
+    byte = _types()[4]
+    if not isinstance(workspace, _TENSOR):
         raise ValueError(f"{where}: workspace must be a tensor")
-    return "workspace", workspace, _types()[4], workspace.numel()
+    return "workspace", workspace, byte, workspace.numel()
 
 
 def _rows(where, name, t, layer):
@@ -600,7 +601,7 @@ class Mx8Weights(ctypes.Structure):
 
 def _mx8_specs(cfg, weights):
     _, _, _, q8, byte = _types()
-    if len(weights) != 6:
+    if not isinstance(weights, (tuple, list)) or len(weights) != 6:
         raise ValueError("weights: (gate, gate_scales, up, up_scales, down, down_scales)")
     n = cfg.E * cfg.D * cfg.F
     return [(name, t, byte if i & 1 else q8, n // 32 if i & 1 else n)
@@ -673,6 +674,8 @@ def moe_balance_loss(cfg, logits, topk_ids, seq_starts, counts, losses, seq_loss
     c_balance * balance + c_z * z (include/moe.h)."""
     _, f32, i32, _, byte = _types()
     T, E = cfg.T, cfg.E
+    if not isinstance(seq_starts, _TENSOR) or seq_starts.numel() < 2:
+        raise ValueError("moe_balance_loss: seq_starts must be a tensor of S + 1 >= 2 borders")
     S = seq_starts.numel() - 1
     dev, p = _check_tensors("moe_balance_loss", (
         ("logits", logits, f32, T * E), ("topk_ids", topk_ids, i32, T * cfg.K),

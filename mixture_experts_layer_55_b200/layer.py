@@ -295,6 +295,8 @@ class MoELayer:
         moe_get_device_status(result["workspace"]).  On the current stream."""
         if getattr(self, "_train_x", None) is None:
             raise RuntimeError("balance_loss() needs a forward_train() first")
+        if not isinstance(seq_starts, torch.Tensor) or seq_starts.numel() < 2:
+            raise ValueError("balance_loss: seq_starts must be a tensor of S + 1 >= 2 borders")
         T, E, K, S = self.cfg.T, self.cfg.E, self.cfg.K, seq_starts.numel() - 1
         lo, io = B.train_state_router(self.cfg)
         logits = self.state[lo:lo + 4 * T * E].view(torch.float32)

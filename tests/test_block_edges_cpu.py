@@ -117,3 +117,20 @@ def test_block_refuses_outputs_over_what_it_still_needs(lib):
     dx = torch.zeros_like(x)
     with pytest.raises(ValueError, match="ds must not be"):
         layer.backward_block(torch.zeros_like(x), ds=dx, grads={"dx": dx})
+
+
+def test_arguments_that_are_no_tensors_are_refused_by_name(lib):
+    c = B.MoeConfig.make(4, 64, 64, 8, 2, "bf16")
+    x, i = torch.zeros(4, 64), torch.zeros(4, 2, dtype=torch.int32)
+    for ws in (None, [0], 4096):
+        with pytest.raises(ValueError, match="workspace must be a tensor"):
+            B.moe_rmsnorm_backward(x, x, torch.ones(64), torch.ones(4), x, torch.ones(64), ws)
+    for starts in (None, [0, 4], torch.zeros(1, dtype=torch.int32), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="seq_starts must be"):
+            B.moe_balance_loss(c, torch.zeros(4, 8), i, starts, i, x, x, torch.zeros(64, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="weights"):
+        B.moe_expert_ffn_mx8(c, x, x, i, None, None, None, x, x, x, torch.zeros(64, dtype=torch.uint8))
+    layer = _layer()
+    layer._train_x = x
+    with pytest.raises(ValueError, match="seq_starts must be"):
+        layer.balance_loss([0, 4])
