@@ -7,6 +7,8 @@ calls ``moe_forward`` (inference), or ``moe_forward_train`` and
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _binding as B
@@ -87,6 +89,13 @@ class MoELayer:
         for i, w in enumerate((self.w_gate, self.w_up, self.w_down)):
             B.moe_mx8_prepare_weight(w, self.mx8[2 * i], self.mx8[2 * i + 1], stream=stream)
 
+    def _on_device(self):
+        """The layer's device as the current one, for calls that go to the current
+        device and its current stream."""
+        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(self.device)
+
     def _terms(self, stream=None):
         if self.router_terms is None:
             return None
@@ -114,12 +123,13 @@ class MoELayer:
         return y
 
     def _forward_mx8(self, x, y, logit_noise=None, stats=True, stream=None, xq=None, xs=None):
-        B.moe_forward_mx8(self.cfg, x, self.w_router, self.mx8, y, self.workspace, xq=xq, xs=xs,
-                          w_router_terms=self._terms(stream), router_bias=self.router_bias,
-                          logit_noise=logit_noise, selection_bias=self.selection_bias,
-                          losses=self.losses if stats else None,
-                          mean_prob=self.mean_prob if stats else None,
-                          counts=self.counts if stats else None, stream=stream)
+        with self._on_device():
+            B.moe_forward_mx8(self.cfg, x, self.w_router, self.mx8, y, self.workspace, xq=xq, xs=xs,
+                              w_router_terms=self._terms(stream), router_bias=self.router_bias,
+                              logit_noise=logit_noise, selection_bias=self.selection_bias,
+                              losses=self.losses if stats else None,
+                              mean_prob=self.mean_prob if stats else None,
+                              counts=self.counts if stats else None, stream=stream)
         return y
 
     def _check_rows(self, where, logit_noise=None, **rows):
@@ -156,7 +166,8 @@ class MoELayer:
         if self.mx8 is not None:
             self._forward_mx8(n, y, logit_noise, stats, xq=q, xs=qs)
         else:
-            self.forward(n, y, logit_noise=logit_noise, stats=stats)
+            with self._on_device():
+                self.forward(n, y, logit_noise=logit_noise, stats=stats)
         return y, s
 
     def capture(self, x, y, logit_noise=None, stats: bool = True):
@@ -261,7 +272,8 @@ class MoELayer:
         if self.mx8 is not None:
             raise ValueError("8-bit experts are for inference: train a layer without them")
         n, s, _, _, rstd = self._norm("forward_block_train", x, residual, y, logit_noise, keep=True)
-        y = self.forward_train(n, y, logit_noise=logit_noise)
+        with self._on_device():
+            y = self.forward_train(n, y, logit_noise=logit_noise)
         self._block = (s, rstd)
         return y, s
 
@@ -276,7 +288,8 @@ class MoELayer:
         if grads is not None and _same(ds, grads["dx"]):
             raise ValueError("backward_block: ds must not be grads' dx, which is written before ds is read")
         self._check_rows("backward_block", dy=dy, ds=ds)
-        grads = self.backward(dy, c_balance, c_z, grads, dlogits_add=dlogits_add)
+        with self._on_device():
+            grads = self.backward(dy, c_balance, c_z, grads, dlogits_add=dlogits_add)
         if "dgamma" not in grads:
             grads["dgamma"] = torch.empty(s.shape[1], dtype=torch.float32, device=s.device)
         if getattr(self, "norm_workspace", None) is None:

@@ -134,3 +134,44 @@ def test_arguments_that_are_no_tensors_are_refused_by_name(lib):
     layer._train_x = x
     with pytest.raises(ValueError, match="seq_starts must be"):
         layer.balance_loss([0, 4])
+
+
+def test_block_runs_on_the_layers_device(lib, monkeypatch):
+    """A layer on a device that is not the current one: every call of its block paths is
+    made with the layer's device current (the norm and the layer on one stream)."""
+    layer = _layer()
+    current, log = [0], []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d.index
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.d
+
+        def __exit__(self, *a):
+            current[0] = self.old
+
+    class Where:
+        type, index = "cuda", 3
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(layer, "device", Where())
+    monkeypatch.setattr(layer, "_check_rows", lambda *a, **k: None)
+    layer.state = layer.bwd_workspace = layer.norm_workspace = torch.zeros(8, dtype=torch.uint8)
+    # the norm goes to its tensors' device by itself
+    monkeypatch.setattr(B, "moe_rmsnorm", lambda *a, **k: None)
+    monkeypatch.setattr(B, "moe_rmsnorm_backward", lambda *a, **k: None)
+    for name in ("moe_forward", "moe_forward_train", "moe_backward", "moe_forward_mx8", "moe_router_prepare"):
+        monkeypatch.setattr(B, name, lambda *a, _n=name, **k: log.append((_n, current[0])))
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    grads = dict.fromkeys(("dw_router", "dw_gate", "dw_up", "dw_down"), x)
+    layer.forward_block(x)
+    layer.forward_block_train(x, x.clone())
+    layer.backward_block(x.clone(), grads=dict(grads, dx=torch.zeros_like(x), dgamma=torch.zeros(64)))
+    layer.mx8 = (x,) * 6
+    layer.forward_block(x)
+    layer.forward(x)
+    names = [n for n, _ in log if n != "moe_router_prepare"]
+    assert names == ["moe_forward", "moe_forward_train", "moe_backward", "moe_forward_mx8", "moe_forward_mx8"]
+    assert {d for _, d in log} == {3} and current == [0]
