@@ -453,6 +453,8 @@ def _nbytes(t) -> int:
 def _check_tensors(where, specs):
     """specs: (name, tensor or None, dtypes, elements).  Returns the device index the
     tensors share and their addresses (None for None)."""
+    if _TYPES is None:
+        _types()
     dev = None
     ptrs = []
     for name, t, dtypes, numel in specs:

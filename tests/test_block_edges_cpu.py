@@ -175,3 +175,11 @@ def test_block_runs_on_the_layers_device(lib, monkeypatch):
     names = [n for n, _ in log if n != "moe_router_prepare"]
     assert names == ["moe_forward", "moe_forward_train", "moe_backward", "moe_forward_mx8", "moe_forward_mx8"]
     assert {d for _, d in log} == {3} and current == [0]
+
+
+def test_block_as_the_first_call_of_a_process(lib, monkeypatch):
+    """The tensors of a first call are told from other objects like any later call's."""
+    monkeypatch.setattr(B, "_TYPES", None)
+    monkeypatch.setattr(B, "_TENSOR", ())
+    with pytest.raises(ValueError, match="CUDA device"):
+        _layer().forward_block(torch.zeros(4, 64, dtype=torch.bfloat16))
