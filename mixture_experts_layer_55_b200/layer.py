@@ -92,7 +92,7 @@ class MoELayer:
     def _on_device(self):
         """The layer's device as the current one, for calls that go to the current
         device and its current stream."""
-        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
+        if self.device.type != "cuda" or torch._C._cuda_getDevice() == self.device.index:
             return contextlib.nullcontext()
         return torch.cuda.device(self.device)
 
@@ -146,7 +146,8 @@ class MoELayer:
             raise ValueError("the layer has no norm_weight")
         if residual is None and _same(x, y):
             raise ValueError(f"{where}: y must not be x, which is the sum the call returns")
-        self._check_rows(where, logit_noise, x=x, residual=residual, y=y)
+        if self.mx8 is None:  # (moe_forward_mx8 checks its tensors itself)
+            self._check_rows(where, logit_noise, x=x, residual=residual, y=y)
         n = torch.empty_like(x)
         s = torch.empty_like(x) if residual is not None else None
         q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if bits8 else None
