@@ -94,13 +94,11 @@ def test_block_refuses_what_is_not_a_whole_batch(lib):
             call(good, logit_noise=torch.zeros(7))
         with pytest.raises(ValueError, match="CUDA device"):
             call(good)
-    # 8-bit experts: by the call that takes them
-    layer.mx8 = tuple(torch.zeros(1, dtype=torch.uint8) for _ in range(6))
-    for x, y, what in ((good[:3], good.clone(), "x has 192"), (good, good[:3].clone(), "y has 192"),
-                       (good.float(), good.clone(), "x has dtype")):
+    # with 8-bit experts: by the call that takes them
+    w = (torch.zeros(1, dtype=torch.uint8),) * 6
+    for x, y, what in ((good[:3], good, "x has 192"), (good, good[:3], "y has 192"), (good.float(), good, "x has dtype")):
         with pytest.raises(ValueError, match=f"moe_forward_mx8: {what}"):
-            layer._forward_mx8(x, y)
-    layer.mx8 = None
+            B.moe_forward_mx8(layer.cfg, x, layer.w_router, w, y, layer.workspace)
     layer._block = (good, torch.ones(4))
     for name in ("dy", "ds"):
         for what, t in bad.items():
