@@ -132,6 +132,33 @@ MOE_DEVICE void bal_wait(const BalArgs& a, uint32_t n)
     __syncthreads();
 }
 
+// Reads of what other blocks have written in this launch: the compiler keeps them
+// behind the wait that they follow.
+MOE_DEVICE int bal_read(const int* p)
+{
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+MOE_DEVICE unsigned long long bal_read(const unsigned long long* p)
+{
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+MOE_DEVICE double bal_read(const double* p)
+{
+    double v;
+    asm volatile("ld.relaxed.gpu.global.f64 %0, [%1];" : "=d"(v) : "l"(p) : "memory");
+    return v;
+}
+MOE_DEVICE int4 bal_read(const int4* p)
+{
+    int4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 template <int L> MOE_DEVICE float group_sum(float v)
 {
 #pragma unroll
@@ -146,7 +173,13 @@ template <int L> MOE_DEVICE float group_max(float v)
 }
 
 // A lane's experts: 8 consecutive ones (rows of a multiple of 4: two 16-byte
-// vectors), or every L-th.
+// vectors), or every L-th; of the logits, or of a row of counts, which this launch
+// writes.
+MOE_DEVICE int4 bal_get4(const float* p) { return __ldcg(reinterpret_cast<const int4*>(p)); }
+MOE_DEVICE int4 bal_get4(const int* p) { return bal_read(reinterpret_cast<const int4*>(p)); }
+MOE_DEVICE float bal_get(const float* p) { return __ldcg(p); }
+MOE_DEVICE int bal_get(const int* p) { return bal_read(p); }
+
 template <int L, bool VEC, typename V>
 MOE_DEVICE void bal_load(const V* row, int lg, int E, V (&v)[kBalPer], V pad)
 {
@@ -155,7 +188,7 @@ MOE_DEVICE void bal_load(const V* row, int lg, int E, V (&v)[kBalPer], V pad)
         for (int q = 0; q < 2; ++q) {
             const int e = lg * kBalPer + 4 * q;
             if (e < E) {
-                const int4 w = __ldcg(reinterpret_cast<const int4*>(row + e));
+                const int4 w = bal_get4(row + e);
                 const int x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[4 * q + i] = *reinterpret_cast<const V*>(&x[i]);
@@ -168,7 +201,7 @@ MOE_DEVICE void bal_load(const V* row, int lg, int E, V (&v)[kBalPer], V pad)
 #pragma unroll
         for (int j = 0; j < kBalPer; ++j) {
             const int e = lg + L * j;
-            v[j] = e < E ? __ldcg(row + e) : pad;
+            v[j] = e < E ? bal_get(row + e) : pad;
         }
     }
 }
@@ -294,7 +327,7 @@ template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThrea
     int my_used = 0;
     unsigned long long my_all = 0;
     for (int k = tid; k < a.S; k += kBalThreads) {
-        const int n = __ldcg(&a.w.tokens[k]);
+        const int n = bal_read(&a.w.tokens[k]);
         my_used += n > 0;
         my_all += n;
     }
@@ -342,7 +375,7 @@ template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThrea
             if (acc != 0) atomicAdd(&a.w.acc[i_of], acc);
             acc = 0;
             i_of = i;
-            inv_n = 1.f / (float)__ldcg(&a.w.tokens[i]);
+            inv_n = 1.f / (float)bal_read(&a.w.tokens[i]);
             const float fscale = inv_n / (float)a.K;
             int n[kBalPer];
             bal_load<L, VEC, int>(a.counts + (int64_t)i * E, lg, E, n, 0);
@@ -420,10 +453,10 @@ template <int L, bool VEC, bool SIG> __global__ void __launch_bounds__(kBalThrea
     if (!sh.last) return;
     // the block that finishes last: per-sequence losses, then both means
     double zsum = 0.0, bsum = 0.0;
-    for (int64_t b = tid; b < gridDim.x; b += kBalThreads) zsum += __ldcg(&a.w.zpart[b]);
+    for (int64_t b = tid; b < gridDim.x; b += kBalThreads) zsum += bal_read(&a.w.zpart[b]);
     for (int64_t k = tid; k < a.S; k += kBalThreads) {
-        const int n = __ldcg(&a.w.tokens[k]), bad = __ldcg(&a.w.bad[k]);
-        const unsigned long long sum = __ldcg(&a.w.acc[k]);
+        const int n = bal_read(&a.w.tokens[k]), bad = bal_read(&a.w.bad[k]);
+        const unsigned long long sum = bal_read(&a.w.acc[k]);
         double v = 0.0;
         if (n > 0) v = bad ? (double)NAN : (double)E * (double)sum / (double)a.fix / (double)n;
         a.seq_loss[k] = (float)v;

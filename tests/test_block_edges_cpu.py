@@ -188,3 +188,15 @@ def test_block_as_the_first_call_of_a_process(lib, monkeypatch):
     monkeypatch.setattr(B, "_TENSOR", ())
     with pytest.raises(ValueError, match="CUDA device"):
         _layer().forward_block(torch.zeros(4, 64, dtype=torch.bfloat16))
+
+
+def test_balance_reads_other_blocks_results_behind_its_waits():
+    """What the balance kernel's blocks write for each other is read by loads that the
+    compiler may not move over a wait; the logits, written by nobody, by any."""
+    with open(os.path.join(CSRC, "balance.cu")) as f:
+        text = f.read()
+    assert {re.sub(r"\s+", " ", line).strip() for line in text.splitlines() if "__ldcg(" in line} == {
+        "MOE_DEVICE int4 bal_get4(const float* p) { return __ldcg(reinterpret_cast<const int4*>(p)); }",
+        "MOE_DEVICE float bal_get(const float* p) { return __ldcg(p); }"}
+    loads = re.findall(r'asm volatile\("ld\.relaxed\.gpu[^;]*;"[^;]*;', text)
+    assert len(loads) == 4 and all('"memory"' in x for x in loads)
