@@ -322,3 +322,44 @@ def test_layer_balance_loss_shows_malformed_borders():
     assert B.moe_get_device_status(again["workspace"]) == 0
     for k in ("losses", "seq_loss", "counts", "dlogits"):
         assert torch.equal(again[k], want[k])
+
+
+def test_norm_in_graphs_of_any_shape():
+    """The norm, which is launched under the end of what stands before it, captured as
+    a graph's first node, behind a copy and a fill, behind two branches, and on two
+    branches at once: what it reads has been written at each replay."""
+    g = _gen(9)
+    T, D = 64, 512
+    x, src, other = (_randn(g, T, D) for _ in range(3))
+    gamma = torch.ones(D, device="cuda")
+    n, n2 = torch.empty_like(x), torch.empty_like(x)
+    for kind in ("first", "copy", "fill", "two branches before", "two branches"):
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            cur = torch.cuda.current_stream()
+            if kind == "copy":
+                x.copy_(src)
+            elif kind == "fill":
+                x.fill_(2.0)
+            elif kind == "two branches before":
+                side.wait_stream(cur)
+                with torch.cuda.stream(side):
+                    x.copy_(src)
+                    x.mul_(2)
+                other.copy_(src)
+                cur.wait_stream(side)
+            elif kind == "two branches":
+                x.mul_(1.5)
+                side.wait_stream(cur)
+                with torch.cuda.stream(side):
+                    M.moe_rmsnorm(x, gamma, n2)
+            M.moe_rmsnorm(x, gamma, n)
+            if kind == "two branches":
+                cur.wait_stream(side)
+        for _ in range(3):
+            src.normal_(generator=g)
+            graph.replay()
+            torch.cuda.synchronize()
+            ref = x.double() * (x.double().square().mean(1, keepdim=True) + 1e-6).rsqrt()
+            within(n, ref, (2.0**-24 + SUM) * ref.abs(), kind)
+            assert kind != "two branches" or torch.equal(n, n2)
