@@ -27,10 +27,10 @@
 // tokens, a token a group of L lanes with 8 experts each, so that a warp is full
 // for 8 experts as for 256.  Bound: latency (launch, two barriers, a handful of
 // dependent loads) up to a few megabytes of logits, then the instructions of a
-// token's softmax.  Measured (softmax, gradient; in us): T = 8192, E = 8, 4
-// sequences 10.3; T = 32768, E = 256, 16 sequences 25.2 (its logits and gradient
-// take 10.2 at the measured copy bandwidth).  As three launches, with a warp per
-// token: 30 and 64.
+// token's softmax.  Measured (with the gradient; in us): T = 8192, E = 8, 4
+// sequences 10.4; T = 32768, E = 256, 16 sequences 25.9 (its logits and gradient
+// take 10.2 at the measured copy bandwidth); T = 16384, E = 64, sigmoid, 37
+// sequences 15.7.  The first two as three launches, with a warp per token: 30 and 64.
 #include "internal.h"
 #include "common.cuh"
 

@@ -64,8 +64,8 @@ constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 2 + SF_WARPS;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int MAX_E = 256;
-// Average rows per expert up to which tokens are the MMA's columns.  Measured
-// (8 experts, D = 4096, F = 14336; as columns and as rows): 16 rows 227 and 244 us,
+// Average rows per expert up to which tokens are the MMA's columns.  Measured on
+// balanced loads (8 experts, D = 4096, F = 14336; as columns and as rows): 16 rows 227 and 244 us,
 // 32 rows 271 and 244; 64 experts, D = 2048, F = 1408: 6 rows 97 and 100, 24 rows
 // 101 and 105, 32 rows 105 and 104, 48 rows 121 and 106.
 constexpr int kFewRows = 24;
